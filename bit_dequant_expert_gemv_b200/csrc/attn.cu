@@ -6,8 +6,8 @@
 //   sum_t p_t v_hat = sum over groups of  sum_t (p_t s_t) code_t + sum_t p_t z_t
 // so that both products multiply the codes themselves. A code's four bits, masked in place, ARE a
 // binary16 number: code * 2^-24 (bits 0..3) or code * 2^-20 (bits 4..7), both subnormal and exact, so
-// unpacking is one AND per two codes and one shift per eight; the powers of two go into q and out. (For binary32
-// activations one more instruction makes them normal numbers.)
+// unpacking is one AND per two codes and one shift per eight; the powers of two go into q and out. (For binary16 and
+// binary32 results one more instruction makes them normal numbers.)
 //
 // One warp takes 16 positions at a time, as the ROWS of m16n8k16 products, 8 query rows as the
 // columns: the heads that share a kv head fill a tile without waste at 8, and the scores come out
@@ -180,6 +180,21 @@ constexpr int kLift = 8, kSlack = 6;
 constexpr int kMinE = kLift;
 constexpr int kShort = 8;  // stages of a ring that are not worth sharing
 
+// How the operands of the two products are held for results of type T, beside sums of binary32.
+//   q: binary16 parts of a query. One holds a 16-bit query as it is, two a binary32 one (22 bits).
+//   ps: binary16 parts of p s. One (2^-12) is far below a bfloat16 result's own rounding of 2^-8. A binary16 result's is
+//     2^-11: one part more than doubled its error, as p s multiplies codes of mean 7.5 that the biases take back out (64
+//     to 20000 positions of like weight: 4.3e-4 to 4.9e-4 in one part, 2.0e-4 to 2.2e-4 in two, which is the rounding
+//     of the result; 12 requests of 5 queries, 64 columns: 38.3 us in one part, 42.7 us in two).
+//   normal: codes as normal numbers. Sums of products drop what lies below 2^-24 of the largest exponent among them, and
+//     a subnormal counts there as 2^10 times what it is: with codes in place a binary32 result was up to 4e-5 off.
+template <typename T>
+struct Held {
+  static constexpr int q = sizeof(T) == 4 ? 2 : 1, ps = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;
+  static constexpr bool normal = ps == 2;
+};
+int terms_of(int dtype) { return dtype == FMOE_F32 ? 2 : 1; }  // Held::q
+
 // CTAs of an SM, by the registers that their sums take.
 __host__ __device__ constexpr int resident(int ng, int nt, int terms) {
   return ng * nt * terms <= 2 ? 4 : ng * nt * terms <= 3 ? 3 : 2;
@@ -187,20 +202,18 @@ __host__ __device__ constexpr int resident(int ng, int nt, int terms) {
 // Tiles of 8 rows that a warp can carry.
 __host__ __device__ constexpr int most_tiles(int ng) { return ng == 1 ? 4 : ng == 2 ? 3 : 2; }
 
-// Two codes as they go into a product: in place (TERMS 1), or as normal numbers. Sums of products drop what lies
-// below 2^-24 of the largest exponent among them, and a subnormal counts there as 2^10 times what it is: with codes
-// in place a binary32 result was up to 4e-5 off.
-template <int TERMS>
+// Two codes as they go into a product.
+template <bool NORMAL>
 __device__ __forceinline__ uint32_t codes_in(uint32_t masked) {
-  if (TERMS == 1) return masked;
+  if (!NORMAL) return masked;
   uint32_t d;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(masked | 0x64006400u), "r"(0x64006400u));  // 1024 + code, exact
   return d;
 }
-// TERMS: 1 rounds p s to binary16 (2^-12 relative), far below the rounding of a 16-bit result; 2 holds
-// q and p s in two binary16 parts (22 bits), for binary32 activations.
-template <typename T, int NG, int NT, int TERMS>
-__global__ void __launch_bounds__(kThreads, resident(NG, NT, TERMS)) attn_kernel(const AttnRun r) {
+template <typename T, int NG, int NT>
+__global__ void __launch_bounds__(kThreads, resident(NG, NT, Held<T>::q)) attn_kernel(const AttnRun r) {
+  constexpr int TERMS = Held<T>::q, PS = Held<T>::ps;
+  constexpr bool NORMAL = Held<T>::normal;
   constexpr int D = NG * 64, MT = NG * 4;
   constexpr int ROWS = 8 * NT;  // of a warp
   using L = Stage<NG>;
@@ -337,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, TERMS)) attn_kernel
     }
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if ((w & 7) == 0) q_stat[rr * (NG + 1) + (w >> 3)] = sum * (TERMS == 1 ? 5.9604644775390625e-8f : 1.0f);  // as the codes: 2^-24
-    if (w == 0) q_stat[rr * (NG + 1) + NG] = fmaxf(pow2i(e) * fabsf(r.a.scale) * (TERMS == 1 ? kLog2e * 16777216.0f : kLog2e), 1e-37f);
+    if ((w & 7) == 0) q_stat[rr * (NG + 1) + (w >> 3)] = sum * (NORMAL ? 1.0f : 5.9604644775390625e-8f);  // as the codes: 2^-24
+    if (w == 0) q_stat[rr * (NG + 1) + NG] = fmaxf(pow2i(e) * fabsf(r.a.scale) * (NORMAL ? kLog2e : kLog2e * 16777216.0f), 1e-37f);
     // codes j, j+4 of a word share a register; odd ones stand 4 bits higher: 16 times larger
     uint32_t a[4], b[4];
 #pragma unroll
@@ -441,8 +454,8 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, TERMS)) attn_kernel
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const uint32_t a = (w ? k[p][0].y : k[p][0].x) >> (8 * u), b = (w ? k[p][1].y : k[p][1].x) >> (8 * u);
-            const uint32_t a0 = codes_in<TERMS>(a & 0x000f000fu), a1 = codes_in<TERMS>(b & 0x000f000fu);
-            const uint32_t a2 = codes_in<TERMS>(a & 0x00f000f0u), a3 = codes_in<TERMS>(b & 0x00f000f0u);
+            const uint32_t a0 = codes_in<NORMAL>(a & 0x000f000fu), a1 = codes_in<NORMAL>(b & 0x000f000fu);
+            const uint32_t a2 = codes_in<NORMAL>(a & 0x00f000f0u), a3 = codes_in<NORMAL>(b & 0x00f000f0u);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -545,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, TERMS)) attn_kernel
       for (int y = 0; y < NG; ++y) {
         const float s0 = scale_of(vs[p][0][y]) * lift, z0 = bias_of(vs[p][0][y]);
         const float s1 = scale_of(vs[p][1][y]) * lift, z1 = bias_of(vs[p][1][y]);
-        uint32_t b[NT][2][TERMS];
+        uint32_t b[NT][2][PS];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float* const q = x[n][p];
@@ -555,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, TERMS)) attn_kernel
           const uint32_t lo = pack_half2(w0, w1), hi = pack_half2(w2, w3);
           b[n][0][0] = transpose8(lo);
           b[n][1][0] = transpose8(hi);
-          if (TERMS == 2) {
-            b[n][0][TERMS - 1] = transpose8(rest_half2(w0, w1, lo));
-            b[n][1][TERMS - 1] = transpose8(rest_half2(w2, w3, hi));
+          if (PS == 2) {
+            b[n][0][PS - 1] = transpose8(rest_half2(w0, w1, lo));
+            b[n][1][PS - 1] = transpose8(rest_half2(w2, w3, hi));
           }
         }
         // values: rows g (codes 0..3 of a word) and g+8 (codes 4..7), columns the positions
@@ -570,13 +583,13 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, TERMS)) attn_kernel
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const uint32_t mask = (t & 1) ? 0x00f000f0u : 0x000f000fu;
-          const uint32_t m0 = codes_in<TERMS>(a0 & mask), m1 = codes_in<TERMS>(a1 & mask);
-          const uint32_t m2 = codes_in<TERMS>(a2 & mask), m3 = codes_in<TERMS>(a3 & mask);
+          const uint32_t m0 = codes_in<NORMAL>(a0 & mask), m1 = codes_in<NORMAL>(a1 & mask);
+          const uint32_t m2 = codes_in<NORMAL>(a2 & mask), m3 = codes_in<NORMAL>(a3 & mask);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < TERMS; ++e)
-              if (TERMS == 1) {
+            for (int e = 0; e < PS; ++e)
+              if (PS == 1) {
                 mma(o[n][4 * y + t], m0, m1, m2, m3, b[n][0][e], b[n][1][e]);
               } else {  // added outside, rounded to nearest: the products' own sums drop what does not fit
                 float part[4];
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, TERMS)) attn_kernel
   // ---- this warp's rows into shared memory: sums over positions (lanes of one c), then out = 2^24-fold codes + biases
   float* const smem = reinterpret_cast<float*>(ring);
   float* const to_rows = smem + warp * ROWS * D;
-  const float f = pow2i(min(E, 254) - 127), up = (TERMS == 1 ? 16777216.0f : 1.0f) / (1 << kLift);
+  const float f = pow2i(min(E, 254) - 127), up = (NORMAL ? 1.0f : 16777216.0f) / (1 << kLift);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -736,8 +749,7 @@ __global__ void __launch_bounds__(D < 128 ? 128 : D) attn_join(const AttnRun r) 
 
 template <typename T, int NG, int NT>
 cudaError_t run(const AttnRun& r, cudaStream_t st) {
-  constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
-  const auto kernel = attn_kernel<T, NG, NT, TERMS>;
+  const auto kernel = attn_kernel<T, NG, NT>;
   const int smem = r.p.smem;
   if (smem > 32 * 1024) {  // with the static part, 48 KB need no leave
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -752,7 +764,7 @@ cudaError_t run(const AttnRun& r, cudaStream_t st) {
 AttnPlan plan_attn(const fmoe_kv_cache& c, const fmoe_attn_desc& a, int sms) {
   AttnPlan p;
   const long long rows = (long long)a.max_q * (a.heads_q / c.heads), tiles = (rows + 7) / 8;
-  const int terms = a.dtype == FMOE_F32 ? 2 : 1, groups = c.dim / 64;
+  const int terms = terms_of(a.dtype), groups = c.dim / 64;
   // as few warps as can carry the rows, and then as few tiles a warp as that takes: what unpacking codes costs is
   // shared by more rows, and more warps have positions of their own. 12 requests of 5 queries, 4 heads a kv head of
   // 64: 37.4 us by three tiles of one warp, 41.2 by three warps; 16 heads a kv head of 256, 262144 positions: 71.3

@@ -1,0 +1,69 @@
+"""GPU: the token mixers at what a norm over a whole result does not see: values that are not finite, results as a
+whole against their correctly rounded values, tokens and heads one by one, calls from several threads and streams."""
+import numpy as np
+import pytest
+import torch
+
+import mixer_reference as ref
+from test_gpu_mixers import DT, cache_of, fmoe  # noqa: F401 (fmoe: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def flips(got, want, dtype, b, what):
+    """`got` against `want` (binary64) rounded to `dtype`, 2-norms over the last axis and all before it.
+
+    A value that is off by d before its rounding lands on the neighbour of the right result with probability d / step,
+    and is then off by a step: the square of the difference is the sum of step * |d| on average, at most |step| |d| in
+    2-norms. With |d| <= b |want| and steps of eps |want| at most that is eps b |want|^2; twice the root for the spread."""
+    rounded = torch.from_numpy(want).to(dtype).double().numpy()
+    off = np.linalg.norm(ref.f64(got) - rounded) / np.linalg.norm(want)
+    bound = 2 * (torch.finfo(dtype).eps * b) ** 0.5
+    assert off <= bound, f"{what}: {off:.3e} > {bound:.3e}"
+
+
+# ------------------------------------------------------------------------------------------------ attention
+def unpacked(pages, ps, d):
+    """Pages of one kv head [pages, bytes] on the GPU -> keys, values [positions, d] in binary64."""
+    codes = pages[:, :ps * d].reshape(-1, 2, ps, d // 2)
+    q = torch.stack([codes & 15, codes >> 4], -1).reshape(-1, 2, ps, d // 64, 64).double()
+    sb = pages[:, ps * d:].contiguous().view(torch.bfloat16).view(-1, 2, ps, d // 64, 2).double()
+    x = (q * sb[..., :1] + sb[..., 1:]).reshape(-1, 2, ps, d)
+    return x[:, 0].reshape(-1, d), x[:, 1].reshape(-1, d)
+
+
+def like_weights(fmoe, dtype, n, requests, d, hq):  # noqa: F811
+    """Positions of like weight whose values average out: a result of about |v| / sqrt(n) from terms of |v| / n. Several
+    requests share their pages.
+
+    Before the rounding to 16 bits a result is off, relative to itself, by: probabilities and their products with the
+    scales, 2^-20 with the exponentials (terms of a few |v| / n, independent of one another); and the sums, whose terms
+    come to 2 sqrt(n) results at most, all of one sign, rounded to nearest, 2^-24 with about sqrt(n) / 2 in a row of
+    errors that average out: 2^-24 sqrt(n). For bfloat16 the products with the scales are rounded to binary16: 2^-12 of
+    each of those terms, which come to twice the values."""
+    ps, dt = 64, DT[dtype]
+    pages, table = cache_of([n], 1, d, ps, 51, extra_pages=0)
+    gen = torch.Generator(device="cuda").manual_seed(52)
+    if requests > 1:
+        order = torch.stack([torch.randperm(table.shape[1], generator=gen, device="cuda") for _ in range(requests)])
+        table = table[0][order].contiguous()
+    q = torch.randn(requests, hq, d, generator=gen, device="cuda").to(dt)
+    L = torch.full((requests,), n, dtype=torch.int32, device="cuda")
+    out = fmoe.attn_q4(q, pages, table, L, n, scale=0.3 / d)
+    assert fmoe.sync_status() == 0
+    k, v = unpacked(pages[:, 0][table[0].long()], ps, d)
+    k, v = k[:n], v[:n]
+    want = torch.cat([torch.softmax(q[i].double() @ k.T * (0.3 / d), -1) @ v for i in range(requests)]).cpu().numpy()
+    got = out.view(-1, d)
+    b = 2.0 ** -20 + 2.0 ** -24 * n ** 0.5
+    if dtype == "fp32":
+        off = np.linalg.norm(ref.f64(got) - want) / np.linalg.norm(want)
+        assert off <= 4 * b, (off, 4 * b)
+    else:
+        flips(got, want, dt, b if dtype == "fp16" else 2.0 ** -11 + b, "out")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n,d,hq", [(64, 64, 8), (1000, 128, 16), (20000, 256, 32)], ids=str)
+def test_attention_of_like_weights_as_a_whole(fmoe, dtype, n, d, hq):
+    like_weights(fmoe, dtype, n, 1, d, hq)
