@@ -202,12 +202,16 @@ __host__ __device__ constexpr int resident(int ng, int nt, int terms) {
 // Tiles of 8 rows that a warp can carry.
 __host__ __device__ constexpr int most_tiles(int ng) { return ng == 1 ? 4 : ng == 2 ? 3 : 2; }
 
-// Two codes as they go into a product.
+// Two codes as they go into a product, less `middle` where they are normal numbers: x_hat = (code - 8) s + (z + 8 s), so
+// that the sums of values are of about the results' size and not of the codes' (131072 positions of like weight, 14000 of
+// them in a row: binary32 results 9.8e-5 off without it).
+constexpr int kMiddle = 8;
 template <bool NORMAL>
-__device__ __forceinline__ uint32_t codes_in(uint32_t masked) {
+__device__ __forceinline__ uint32_t codes_in(uint32_t masked, int middle = 0) {
   if (!NORMAL) return masked;
   uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(masked | 0x64006400u), "r"(0x64006400u));  // 1024 + code, exact
+  const uint32_t base = 0x6400u + middle;  // 1024 + code - (1024 + middle), exact
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(masked | 0x64006400u), "r"(base << 16 | base));
   return d;
 }
 template <typename T, int NG, int NT>
@@ -553,12 +557,13 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, Held<T>::q)) attn_k
           }
       }
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int y = 0; y < NG; ++y) {
+      uint32_t b[2][NT][2][PS], a[2][4];
 #pragma unroll
-      for (int y = 0; y < NG; ++y) {
-        const float s0 = scale_of(vs[p][0][y]) * lift, z0 = bias_of(vs[p][0][y]);
-        const float s1 = scale_of(vs[p][1][y]) * lift, z1 = bias_of(vs[p][1][y]);
-        uint32_t b[NT][2][PS];
+      for (int p = 0; p < 2; ++p) {
+        float s0 = scale_of(vs[p][0][y]), z0 = bias_of(vs[p][0][y]), s1 = scale_of(vs[p][1][y]), z1 = bias_of(vs[p][1][y]);
+        if (NORMAL) z0 = fmaf(kMiddle, s0, z0), z1 = fmaf(kMiddle, s1, z1);
+        s0 *= lift, s1 *= lift;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float* const q = x[n][p];
@@ -566,11 +571,11 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, Held<T>::q)) attn_k
           zs[n][y][0] = fmaf(q[0], z0, fmaf(q[2], z1, zs[n][y][0]));
           zs[n][y][1] = fmaf(q[1], z0, fmaf(q[3], z1, zs[n][y][1]));
           const uint32_t lo = pack_half2(w0, w1), hi = pack_half2(w2, w3);
-          b[n][0][0] = transpose8(lo);
-          b[n][1][0] = transpose8(hi);
+          b[p][n][0][0] = transpose8(lo);
+          b[p][n][1][0] = transpose8(hi);
           if (PS == 2) {
-            b[n][0][PS - 1] = transpose8(rest_half2(w0, w1, lo));
-            b[n][1][PS - 1] = transpose8(rest_half2(w2, w3, hi));
+            b[p][n][0][PS - 1] = transpose8(rest_half2(w0, w1, lo));
+            b[p][n][1][PS - 1] = transpose8(rest_half2(w2, w3, hi));
           }
         }
         // values: rows g (codes 0..3 of a word) and g+8 (codes 4..7), columns the positions
@@ -578,28 +583,38 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, Held<T>::q)) attn_k
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           v[j] = *reinterpret_cast<const uint32_t*>(st + L::kV + (16 * p + 4 * j) * L::kRow + value_at(y, j));
-        uint32_t a0 = __byte_perm(v[0], v[1], 0x5410), a1 = __byte_perm(v[0], v[1], 0x7632);
-        uint32_t a2 = __byte_perm(v[2], v[3], 0x5410), a3 = __byte_perm(v[2], v[3], 0x7632);
+        a[p][0] = __byte_perm(v[0], v[1], 0x5410), a[p][1] = __byte_perm(v[0], v[1], 0x7632);
+        a[p][2] = __byte_perm(v[2], v[3], 0x5410), a[p][3] = __byte_perm(v[2], v[3], 0x7632);
+      }
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t mask = (t & 1) ? 0x00f000f0u : 0x000f000fu;
-          const uint32_t m0 = codes_in<NORMAL>(a0 & mask), m1 = codes_in<NORMAL>(a1 & mask);
-          const uint32_t m2 = codes_in<NORMAL>(a2 & mask), m3 = codes_in<NORMAL>(a3 & mask);
+      for (int t = 0; t < 4; ++t) {
+        uint32_t m[2][4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int e = 0; e < PS; ++e)
-              if (PS == 1) {
-                mma(o[n][4 * y + t], m0, m1, m2, m3, b[n][0][e], b[n][1][e]);
-              } else {  // added outside, rounded to nearest: the products' own sums drop what does not fit
-                float part[4];
-                mma_first(part, m0, m1, m2, m3, b[n][0][e], b[n][1][e]);
+          for (int j = 0; j < 4; ++j) {
+            m[p][j] = codes_in<NORMAL>(a[p][j] & ((t & 1) ? 0x00f000f0u : 0x000f000fu), (t & 1) ? kMiddle * 16 : kMiddle);
+            if (t == 1) a[p][j] >>= 8;
+          }
+        // A stage's products are summed by themselves and added outside, rounded to nearest: the products' own sums drop
+        // what does not fit, always to the same side (binary32 results: not even four products are summed so).
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[n][4 * y + t][j] += part[j];
-              }
-          if (t == 1) a0 >>= 8, a1 >>= 8, a2 >>= 8, a3 >>= 8;
+        for (int n = 0; n < NT; ++n) {
+          float part[4];
+#pragma unroll
+          for (int i = 0; i < 2 * PS; ++i) {
+            const int p = i / PS, e = i % PS;
+            if (i == 0 || TERMS == 2)
+              mma_first(part, m[p][0], m[p][1], m[p][2], m[p][3], b[p][n][0][e], b[p][n][1][e]);
+            else
+              mma(part, m[p][0], m[p][1], m[p][2], m[p][3], b[p][n][0][e], b[p][n][1][e]);
+            if (i == 2 * PS - 1 || TERMS == 2)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[n][4 * y + t][j] += part[j];
+          }
         }
       }
+    }
   }
   copy_wait<0>();
   __syncthreads();

@@ -67,3 +67,28 @@ def like_weights(fmoe, dtype, n, requests, d, hq):  # noqa: F811
 @pytest.mark.parametrize("n,d,hq", [(64, 64, 8), (1000, 128, 16), (20000, 256, 32)], ids=str)
 def test_attention_of_like_weights_as_a_whole(fmoe, dtype, n, d, hq):
     like_weights(fmoe, dtype, n, 1, d, hq)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_attention_of_like_weights_in_long_shares(fmoe, dtype):
+    """A warp has about 14000 positions one after another."""
+    like_weights(fmoe, dtype, 131072, 256, 64, 8)
+
+
+@pytest.mark.parametrize("scale", [0.0, 0.088, 2.0])
+def test_attention_long_as_a_whole(fmoe, scale):
+    """Binary32 results over many joined parts, head by head: logits of up to |x| are off by 2^-22 |x| and move every
+    probability by as much, relative; the rest as above."""
+    n, d, ps = 70001, 128, 64
+    pages, table = cache_of([n], 2, d, ps, 9)
+    q = torch.randn(1, 16, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    out = fmoe.attn_q4(q, pages, table, torch.tensor([n], dtype=torch.int32, device="cuda"), n, scale=scale)
+    assert fmoe.sync_status() == 0
+    for h in range(2):
+        k, v = unpacked(pages[:, h][table[0].long()], ps, d)
+        x = q[0, 8 * h:8 * h + 8].double() @ k[:n].T * scale
+        want = (torch.softmax(x, -1) @ v[:n]).cpu().numpy()
+        top = float(x.abs().max())
+        for r in range(8):
+            off = np.linalg.norm(ref.f64(out[0, 8 * h + r]) - want[r]) / np.linalg.norm(want[r])
+            assert off <= 4 * (2.0 ** -20 + 2.0 ** -24 * n ** 0.5 + 2.0 ** -22 * top), (h, r, off)
