@@ -494,7 +494,21 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, Held<T>::q)) attn_k
 #pragma unroll
         for (int y = 0; y < NG; ++y) ts = fmaxf(ts, fabsf(scale_of(vs[p][j][y])));
       }
-    const int top = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(ts)) >> 23), En = top > E ? top + 1 : E;
+    int top = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(ts)) >> 23);
+    if (top == 255) {  // an infinite scale spoils its own 64 columns; the others keep the exponent of what is finite
+      ts = 0.f;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int y = 0; y < NG; ++y) {
+            const float s = fabsf(scale_of(vs[p][j][y]));
+            if (s < INFINITY) ts = fmaxf(ts, s);
+          }
+      top = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(ts)) >> 23);
+    }
+    const int En = top > E ? top + 1 : E;
     if (tail) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)

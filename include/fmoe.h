@@ -423,6 +423,9 @@ int fmoe_kv_read(const fmoe_kv_cache* cache, const int32_t* positions, const int
  * queries sees positions 0 .. lens[i] - n_i + j. Query head h reads kv head h / (heads_q / heads).
  *     out = sum_t p_t v_hat_t,  p = softmax(scale * q . k_hat_t)   over the positions seen
  * A query that sees nothing gives zeros. Softmax statistics and sums are binary32.
+ * What no query sees may hold anything. A key's scale or bias that is seen and not finite makes the
+ * query's results so, a value's those of its 64 columns (all of the query's, where another query of
+ * its sequence does not see that position).
  * max_q, max_len: upper bounds (host) of the queries of a sequence and of lens; a length beyond
  * max_len or the table, or more queries than max_q, is cut and reported as FMOE_ERR_INDEX; a page
  * id out of range is reported and its positions are not seen. */

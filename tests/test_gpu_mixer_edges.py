@@ -22,6 +22,10 @@ def flips(got, want, dtype, b, what):
     assert off <= bound, f"{what}: {off:.3e} > {bound:.3e}"
 
 
+# ------------------------------------------------------------------------------------------------ delta rule
+NAN, INF = float("nan"), float("inf")
+
+
 # ------------------------------------------------------------------------------------------------ attention
 def unpacked(pages, ps, d):
     """Pages of one kv head [pages, bytes] on the GPU -> keys, values [positions, d] in binary64."""
@@ -92,3 +96,21 @@ def test_attention_long_as_a_whole(fmoe, scale):
         for r in range(8):
             off = np.linalg.norm(ref.f64(out[0, 8 * h + r]) - want[r]) / np.linalg.norm(want[r])
             assert off <= 4 * (2.0 ** -20 + 2.0 ** -24 * n ** 0.5 + 2.0 ** -22 * top), (h, r, off)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_attention_values_not_finite(fmoe, dtype, value):
+    """A value scale or bias that is not finite makes its 64 columns so, and no others."""
+    n, d, ps = 100, 128, 16
+    for part in (0, 1):
+        pages, table = cache_of([n], 1, d, ps, 71)
+        clean = pages.clone()
+        sb = pages[:, :, ps * d:].view(torch.bfloat16).view(-1, 1, 2, ps, 2, 2)
+        sb[int(table[0, 0]), 0, 1, 3, 0, part] = value
+        q = torch.randn(1, 4, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(4)).to(DT[dtype])
+        L = torch.tensor([n], dtype=torch.int32, device="cuda")
+        out, want = fmoe.attn_q4(q, pages, table, L, n), fmoe.attn_q4(q, clean, table, L, n)
+        assert fmoe.sync_status() == 0
+        assert not torch.isfinite(out[..., :64]).any()
+        assert torch.equal(out[..., 64:], want[..., 64:])
