@@ -246,6 +246,12 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, Held<T>::q)) attn_k
   };
 
   cudaTriggerProgrammaticLaunchCompletion();  // the joining launch may be set up; it waits for this one's end
+  // Counts and lengths out of range, of sequences without queries too: an item's first CTA, or the first of all.
+  if (r.p.by_item) {
+    if (blockIdx.x % units == 0 && threadIdx.x == 0) seq_of(r, blockIdx.x / units, true);
+  } else if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < r.c.n_seqs; i += kThreads) seq_of(r, i, true);
+  }
   long long now, last;
   Place at;
   if (r.p.by_item) {
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, resident(NG, NT, Held<T>::q)) attn_k
   for (;;) {
   const int i = at.i, h = at.unit / r.p.row_blocks, rb = at.unit - h * r.p.row_blocks;
   const int passes = (int)min((long long)(at.n - at.pass), last - now);  // of this item
-  const Seq s = seq_of(r, i, at.unit == 0 && at.pass == 0 && threadIdx.x == 0);
+  const Seq s = seq_of(r, i, false);
   const int block_row = rb * r.p.row_warps * ROWS, rows = min(s.nq, r.a.max_q) * group;
   if (block_row < rows) {
   const int block_seen = seen(s, min(rows - 1, block_row + r.p.row_warps * ROWS - 1) / group);

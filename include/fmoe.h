@@ -427,8 +427,9 @@ int fmoe_kv_read(const fmoe_kv_cache* cache, const int32_t* positions, const int
  * query's results so, a value's those of its 64 columns (all of the query's, where another query of
  * its sequence does not see that position).
  * max_q, max_len: upper bounds (host) of the queries of a sequence and of lens; a length beyond
- * max_len or the table, or more queries than max_q, is cut and reported as FMOE_ERR_INDEX; a page
- * id out of range is reported and its positions are not seen. */
+ * max_len or the table, or more queries than max_q, is cut and reported as FMOE_ERR_INDEX, of
+ * sequences without queries too; so is a cu_q that falls (rows that two sequences then name hold
+ * either's result). A page id out of range is reported and its positions are not seen. */
 typedef struct fmoe_attn_desc {
     int heads_q;
     int dtype;               /* of q, out                                             */

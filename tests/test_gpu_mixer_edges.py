@@ -114,3 +114,27 @@ def test_attention_values_not_finite(fmoe, dtype, value):
         assert fmoe.sync_status() == 0
         assert not torch.isfinite(out[..., :64]).any()
         assert torch.equal(out[..., 64:], want[..., 64:])
+
+
+@pytest.mark.parametrize("most", [100, 9000])
+def test_attention_counts_that_fall_back(fmoe, most):
+    """A cu_q that falls, and lengths out of range of sequences without queries, are reported, whether thread blocks
+    take whole items (short) or share all passes."""
+    lens, d, ps = [100, 60, 90], 64, 16
+    pages, table = cache_of([9000 if most > 100 else 100, 60, 90], 1, d, ps, 4)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.randn(8, 2, d, generator=gen, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def status(cu, lengths):
+        out = fmoe.attn_q4(q, pages, table, torch.tensor(lengths, **i32), most, cu_q=torch.tensor(cu, **i32), max_q=5)
+        return out, fmoe.sync_status()
+    good, code = status([0, 3, 5, 8], lens)
+    assert code == 0
+    got, code = status([0, 3, 3, 8], lens)
+    assert code == 0 and torch.equal(got[:3], good[:3])
+    for cu, lengths in (([0, 5, 3, 8], lens), ([0, 3, 3, 8], [100, -5, 90]), ([0, 3, 3, 8], [100, 10 ** 6, 90]),
+                        ([0, 8, 8, 2], lens)):
+        _, code = status(cu, lengths)
+        assert code == fmoe.FMOE_ERR_INDEX and "length" in fmoe.last_error(), (cu, lengths)
+    assert fmoe.sync_status() == 0
