@@ -124,8 +124,8 @@ __device__ __forceinline__ Place find_pass(const AttnRun& r, long long at, int u
     const unsigned past = __ballot_sync(0xffffffffu, sum > at);
     if (past) {
       const int l = __ffs(past) - 1, nl = __shfl_sync(0xffffffffu, n, l);
-      const int in = (int)(at - (__shfl_sync(0xffffffffu, sum, l) - (long long)nl * units));
-      return {base + l, in / nl, in % nl, nl};
+      const long long in = at - (__shfl_sync(0xffffffffu, sum, l) - (long long)nl * units);  // may pass 2^31
+      return {base + l, (int)(in / nl), (int)(in % nl), nl};
     }
     at -= __shfl_sync(0xffffffffu, sum, 31);
   }

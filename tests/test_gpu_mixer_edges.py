@@ -138,3 +138,22 @@ def test_attention_counts_that_fall_back(fmoe, most):
         _, code = status(cu, lengths)
         assert code == fmoe.FMOE_ERR_INDEX and "length" in fmoe.last_error(), (cu, lengths)
     assert fmoe.sync_status() == 0
+
+
+def test_attention_of_2_31_passes(fmoe):
+    """More than 2^31 passes: a table that names one page again and again, and a bound of the queries that gives 65520
+    blocks of rows, all empty but one. The result is that of the one page, but for sums of up to 2^17 terms in a row:
+    2^-25 each of up to four results."""
+    d, ps, times = 64, 1024, 1026
+    pages, one = cache_of([ps], 1, d, ps, 81, extra_pages=0)
+    q = torch.randn(1, 2, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6))
+    table = one.expand(1, times).contiguous()
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    n, most = ps * times, 65520 * 128 // 2  # 128 rows of two heads a block
+    assert n // 32 * 65520 > 2 ** 31
+    out = fmoe.attn_q4(q, pages, table, torch.tensor([n], dtype=torch.int32, device="cuda"), n, cu_q=cu, max_q=most, scale=0.2)
+    assert fmoe.sync_status() == 0
+    k, v = unpacked(pages[:, 0], ps, d)
+    want = (torch.softmax(q[0].double() @ k.T * 0.2, -1) @ v).cpu().numpy()
+    off = np.linalg.norm(ref.f64(out[0]) - want) / np.linalg.norm(want)
+    assert off <= 4 * 2.0 ** -8, off
