@@ -782,15 +782,29 @@ __global__ void __launch_bounds__(D < 128 ? 128 : D) attn_join(const AttnRun r) 
   store_f32<T, 4>(static_cast<T*>(r.a.out.ptr) + (s.q0 + j) * r.a.out.token_stride + head * r.a.out.head_stride + 4 * lane, y);
 }
 
+// Shared memory of a thread block: the rings and the queries' fragments, or the warps' results, after the last stage.
+struct Shared {
+  int q_offset, bytes;
+};
+constexpr Shared shared_of(int groups, int row_tiles, int terms, int row_warps) {
+  const int dim = groups * 64, rings = kWarps / row_warps, stage = kStage * (dim + dim / 8);
+  const int q_bytes = row_warps * row_tiles * 8 * (groups * terms * 128 + (groups + 1) * 4);
+  const int out_bytes = kWarps * 8 * row_tiles * dim * 4, q_offset = rings * kStages * stage;
+  return {q_offset, q_offset + q_bytes > out_bytes ? q_offset + q_bytes : out_bytes};
+}
+
 template <typename T, int NG, int NT>
 cudaError_t run(const AttnRun& r, cudaStream_t st) {
   const auto kernel = attn_kernel<T, NG, NT>;
-  const int smem = r.p.smem;
-  if (smem > 32 * 1024) {  // with the static part, 48 KB need no leave
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The limit belongs to the kernel, not to the call: always what its largest launch takes, so that a call of another
+  // host thread never lowers it between this one's setting and launch.
+  constexpr int terms = Held<T>::q, one = shared_of(NG, NT, terms, 1).bytes, two = shared_of(NG, NT, terms, 2).bytes,
+                four = shared_of(NG, NT, terms, 4).bytes, most = one > two ? (one > four ? one : four) : two > four ? two : four;
+  if (most > 32 * 1024) {  // with the static part, 48 KB need no leave
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<r.p.ctas, kThreads, smem, st>>>(r);
+  kernel<<<r.p.ctas, kThreads, r.p.smem, st>>>(r);
   return cudaGetLastError();
 }
 
@@ -810,11 +824,9 @@ AttnPlan plan_attn(const fmoe_kv_cache& c, const fmoe_attn_desc& a, int sms) {
   while (p.row_warps < kWarps && p.row_warps < warps) p.row_warps *= 2;
   p.row_blocks = (int)((warps + p.row_warps - 1) / p.row_warps);
   const int at_once = resident(groups, p.row_tiles, terms);
-  const int rings = kWarps / p.row_warps, stage = kStage * (c.dim + c.dim / 8);
-  const int q_bytes = p.row_warps * p.row_tiles * 8 * (groups * terms * 128 + (groups + 1) * 4);
-  const int out_bytes = kWarps * 8 * p.row_tiles * c.dim * 4;  // the warps' results, after the last stage
-  p.q_offset = rings * kStages * stage;
-  p.smem = std::max(p.q_offset + q_bytes, out_bytes);
+  const int rings = kWarps / p.row_warps;
+  const Shared shared = shared_of(groups, p.row_tiles, terms, p.row_warps);
+  p.q_offset = shared.q_offset, p.smem = shared.bytes;
   const long long units = (long long)c.heads * p.row_blocks;
   const long long items = c.n_seqs * units, passes = std::max(1, (a.max_len + kStage - 1) / kStage);
   // Short sequences: a CTA takes one item, whatever its length, and nothing is left to join. One request of 777

@@ -1,5 +1,8 @@
 """GPU: the token mixers at what a norm over a whole result does not see: values that are not finite, results as a
 whole against their correctly rounded values, tokens and heads one by one, calls from several threads and streams."""
+
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -157,3 +160,36 @@ def test_attention_of_2_31_passes(fmoe):
     want = (torch.softmax(q[0].double() @ k.T * 0.2, -1) @ v).cpu().numpy()
     off = np.linalg.norm(ref.f64(out[0]) - want) / np.linalg.norm(want)
     assert off <= 4 * 2.0 ** -8, off
+
+
+# ------------------------------------------------------------------------------------------------ as they are used
+def test_attention_from_two_threads(fmoe):
+    """Two host threads, each with its stream, whose calls run one kernel with different amounts of shared memory: none
+    is refused, and the results are those of one thread."""
+    d, ps, lens = 256, 64, [200, 130]
+    pages, table = cache_of(lens, 1, d, ps, 91)
+    L = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    cache, calls = fmoe._cache(pages.get_device(), pages, table, d), []
+    for m in (1, 2):  # 16 rows of two tiles: one warp's, two warps'
+        q = torch.randn(2 * m, 16, d, generator=gen, device="cuda").to(torch.bfloat16)
+        cu = torch.tensor([0, m, 2 * m], dtype=torch.int32, device="cuda")
+        want = fmoe.attn_q4(q, pages, table, L, 200, cu_q=cu, max_q=m)
+        out = torch.zeros_like(want)
+        desc = fmoe.AttnDesc(16, fmoe.FMOE_BF16, 2 * m, m, 200, d ** -0.5, q.data_ptr(), 16 * d, d, cu.data_ptr(),
+                             L.data_ptr(), out.data_ptr(), 16 * d, d)
+        calls.append((desc, want, out, q, cu, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    attn, codes = fmoe.lib().fmoe_attn_q4, [set(), set()]
+
+    def work(i):
+        desc, stream = calls[i][0], calls[i][-1].cuda_stream
+        for _ in range(20000):
+            codes[i].add(attn(cache, desc, stream))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert codes == [{0}, {0}] and fmoe.sync_status() == 0, codes
+    torch.cuda.synchronize()
+    for _, want, out, *_ in calls:
+        assert torch.equal(out, want)
