@@ -27,8 +27,9 @@
 // Precision. Operands are binary16 with a power of two taken out of every row: keys and queries (16-bit
 // inputs) are exact to 2^-25 of a row's largest value; binary32 operands (S, the right-hand side, U, T) are
 // split into two binary16 parts, 22 bits, and products of two small parts are left out; norms, decays and
-// gates multiply the binary32 results. M, and U where it meets M, are rounded to binary16 (2^-12): they reach
-// nothing but the 16-bit output. A binary16 output keeps both parts of U there.
+// gates multiply the binary32 results. For a bfloat16 output M, and U where it meets M, are rounded to binary16 (2^-12,
+// its own rounding is 2^-8): they reach nothing but the output. A binary16 output (2^-11) has both parts of M and of
+// U (with M in one its error was 1.4 times the rounding's), and the low parts of S where it meets Q.
 #include "api.h"
 #include "mixer.h"
 #include "mma.cuh"
@@ -53,13 +54,13 @@ template <int DK>
 struct Smem {
   static constexpr int kPanels = DK / 64, kPanel = 128 * 128;  // [K; Q]: 128 rows of 64 columns each
   // a stage: operands; values; for each token e^G a, e^(G_C - G) a and the query's factor; a Scalars
-  static constexpr int kKQ = 0, kTh = kKQ + kPanels * kPanel, kTl = kTh + C * 128, kM = kTl + C * 128;
-  static constexpr int kV = kM + C * 128, kCa = kV + C * 256, kW = kCa + C * 4, kOut = kW + C * 4, kEnd = kOut + C * 4;
+  static constexpr int kKQ = 0, kTh = kKQ + kPanels * kPanel, kTl = kTh + C * 128, kM = kTl + C * 128, kMl = kM + C * 128;
+  static constexpr int kV = kMl + C * 128, kCa = kV + C * 256, kW = kCa + C * 4, kOut = kW + C * 4, kEnd = kOut + C * 4;
   static constexpr int kStage = (kEnd + 32 + 1023) / 1024 * 1024;
-  // behind two stages: rows as they come (32 bytes apart, for the banks), L, the inverse, a product; running
+  // behind two stages: rows as they come (32 bytes apart, for the banks), L and in its place the inverse, a product; running
   // decays with the keys' factors, gates, queries' factors, largest norms and entries, keys' factors with their decay to the end of their 16 tokens, row scales
-  static constexpr int kRow = DK * 2 + 32, kRaw = 2 * kStage, kL = kRaw + 2 * C * kRow, kX = kL + C * LD * 4;
-  static constexpr int kY = kX + C * LD * 4, kG = kY + 32 * 36 * 4, kBeta = kG + C * 16, kA = kBeta + C * 4;
+  static constexpr int kRow = DK * 2 + 32, kRaw = 2 * kStage, kL = kRaw + 2 * C * kRow;
+  static constexpr int kY = kL + C * LD * 4, kG = kY + 32 * 36 * 4, kBeta = kG + C * 16, kA = kBeta + C * 4;
   static constexpr int kB = kA + C * 4, kFall = kB + 128, kRows = kFall + C * 4, kBar = kRows + 128 * 8, kBytes = kBar + 64;
 };
 struct Scalars {
@@ -224,19 +225,20 @@ __device__ __forceinline__ void tile_product(float* y, int ldy, const float* a, 
   *reinterpret_cast<float2*>(y + (g + 8) * ldy + 2 * c) = make_float2(s[2], s[3]);
 }
 
-// X = (I + L)^-1, lower triangle by blocks: the lower left of [[A, 0], [B, D]]^-1 is -D^-1 B A^-1.
-__device__ __forceinline__ void invert(const float* L, float* X, float* Y, int tid) {
+// (I + X)^-1 in the place of X, lower triangle by blocks: the lower left of [[A, 0], [B, D]]^-1 is -D^-1 B A^-1.
+__device__ __forceinline__ void invert(float* X, float* Y, int tid) {
   const int warp = tid >> 5, lane = tid & 31;
   if (warp < 4) {
     // 8 x 8 on the diagonal by substitution, a column each lane; a warp has the two blocks of its 16 rows
     if (lane < 16) {
       const int o = 16 * warp + (lane & 8), c = lane & 7;
-      const float* const l = L + o * LD + o;
+      const float* const l = X + o * LD + o;
       float y[8], x[28];
 #pragma unroll
       for (int i = 1; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < i; ++j) x[i * (i - 1) / 2 + j] = -l[i * LD + j];
+      __syncwarp(0xffffu);  // every lane has read its block
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = i == c ? 1.f : 0.f;
 #pragma unroll
@@ -250,7 +252,7 @@ __device__ __forceinline__ void invert(const float* L, float* X, float* Y, int t
     const int o = 16 * warp, row = lane >> 2, col = 2 * (lane & 3);
     float* const y = Y + warp * 8 * 12;
     float s[1][2] = {};
-    const float* const a[1] = {L + (o + 8 + row) * LD + o};
+    const float* const a[1] = {X + (o + 8 + row) * LD + o};
     small_product<8>(s, a, X + o * LD + o + col, LD);
     *reinterpret_cast<float2*>(y + row * 12 + col) = make_float2(s[0][0], s[0][1]);
     *reinterpret_cast<float2*>(X + (o + row) * LD + o + 8 + col) = make_float2(0.f, 0.f);
@@ -265,7 +267,7 @@ __device__ __forceinline__ void invert(const float* L, float* X, float* Y, int t
     const int pair = warp >> 1 & 1, o = 32 * pair, col = 8 * (warp & 1);
     float* const y = Y + pair * 16 * 20 + col;
     if (warp < 4) {
-      tile_product<16>(y, 20, L + (o + 16) * LD + o, X + o * LD + o + col, LD, 1.f, lane);
+      tile_product<16>(y, 20, X + (o + 16) * LD + o, X + o * LD + o + col, LD, 1.f, lane);
     } else {
       const int x = tid - 128, row = (x & 63) >> 2;
       *reinterpret_cast<float4*>(X + (32 * (x >> 6) + row) * LD + 32 * (x >> 6) + 16 + 4 * (x & 3)) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -276,7 +278,7 @@ __device__ __forceinline__ void invert(const float* L, float* X, float* Y, int t
   bar_sync(kBarAux, kAux);
   {  // 32 and 32: a tile each warp
     const int row = 16 * (warp & 1), col = 8 * (warp >> 1);
-    tile_product<32>(Y + row * 36 + col, 36, L + (32 + row) * LD, X + col, LD, 1.f, lane);
+    tile_product<32>(Y + row * 36 + col, 36, X + (32 + row) * LD, X + col, LD, 1.f, lane);
     bar_sync(kBarAux, kAux);
     tile_product<32>(X + (32 + row) * LD + col, LD, X + (32 + row) * LD + 32, Y + col, 36, -1.f, lane);
   }
@@ -292,7 +294,6 @@ __device__ __forceinline__ void prepare_chunk(const DeltaRun& r, uint8_t* smem, 
   const fmoe_delta_desc& d = r.d;
   const int warp = tid >> 5;
   float* const L = reinterpret_cast<float*>(smem + M::kL);
-  float* const X = reinterpret_cast<float*>(smem + M::kX);
   float4* const G = reinterpret_cast<float4*>(smem + M::kG);  // decay (two parts), key's factor
   const float* const beta = reinterpret_cast<const float*>(smem + M::kBeta);
   float* const qb = reinterpret_cast<float*>(smem + M::kA);
@@ -385,14 +386,21 @@ __device__ __forceinline__ void prepare_chunk(const DeltaRun& r, uint8_t* smem, 
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               h[j] = pack_half2(__uint_as_float(v[8 * q + 2 * j]), __uint_as_float(v[8 * q + 2 * j + 1]));
-            *reinterpret_cast<uint4*>(stage + M::kM + swz(i, (c0 >> 3) + q, 128)) = make_uint4(h[0], h[1], h[2], h[3]);
+            const uint32_t at = swz(i, (c0 >> 3) + q, 128);
+            *reinterpret_cast<uint4*>(stage + M::kM + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (std::is_same<T, __half>::value) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                h[j] = rest_half2(__uint_as_float(v[8 * q + 2 * j]), __uint_as_float(v[8 * q + 2 * j + 1]), h[j]);
+              *reinterpret_cast<uint4*>(stage + M::kMl + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
           }
         }
       }
     }
   }
   bar_sync(kBarAux, kAux);
-  invert(L, X, reinterpret_cast<float*>(smem + M::kY), tid);
+  invert(L, reinterpret_cast<float*>(smem + M::kY), tid);
 
   // ---- T, its columns times beta, in two binary16 parts, a quarter of a row each thread; the tokens' factors
   {
@@ -401,7 +409,7 @@ __device__ __forceinline__ void prepare_chunk(const DeltaRun& r, uint8_t* smem, 
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
       const float4 a = part > 1 && row < 32 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                            : *reinterpret_cast<const float4*>(X + row * LD + 16 * part + j);
+                                            : *reinterpret_cast<const float4*>(L + row * LD + 16 * part + j);
       const float4 b = *reinterpret_cast<const float4*>(beta + 16 * part + j);
       v[j] = a.x * b.x, v[j + 1] = a.y * b.y, v[j + 2] = a.z * b.z, v[j + 3] = a.w * b.w;
       top = fmaxf(top, fmaxf(fmaxf(fabsf(v[j]), fabsf(v[j + 1])), fmaxf(fabsf(v[j + 2]), fabsf(v[j + 3]))));
@@ -740,11 +748,11 @@ __device__ __forceinline__ void chain(const DeltaRun& r, uint8_t* smem, int seq,
     if (threadIdx.x == 0) {
       tc_fence_after();
 #pragma unroll
-      for (int part = 0; part < (kLow ? 2 : 1); ++part)
+      for (int part = 0; part < (kLow ? 3 : 1); ++part)  // high x high, low x high, high x low
 #pragma unroll
         for (int k = 0; k < C / 16; ++k)
-          tc_mma_ts(tmem + kColO, tmem + kColP + part * 16 + 32 * (k >> 1) + 8 * (k & 1), smem_operand(st + M::kM + k * 32), tc_shape(C),
-                    part + k > 0);
+          tc_mma_ts(tmem + kColO, tmem + kColP + (part == 1 ? 16 : 0) + 32 * (k >> 1) + 8 * (k & 1),
+                    smem_operand(st + (part == 2 ? M::kMl : M::kM) + k * 32), tc_shape(C), part + k > 0);
       tc_commit(out_bar);
     }
     __syncwarp();

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import mixer_reference as ref
-from test_gpu_mixers import DT, cache_of, fmoe  # noqa: F401 (fmoe: a fixture)
+from test_gpu_mixers import DT, cache_of, delta_inputs, fmoe, state_bound  # noqa: F401 (fmoe: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -26,6 +26,110 @@ def flips(got, want, dtype, b, what):
 
 
 # ------------------------------------------------------------------------------------------------ delta rule
+def delta_parts(q, k, v, g, beta, S, scale, eps=1e-6):
+    """One sequence as ref.delta, l2norm on, and for each token what its result is summed from: out, state, u,
+    |q~|^T |S| of the state before the token's chunk as far as it has not decayed, and sum |q~ k~| |u| over the tokens
+    of the chunk up to it (both times scale)."""
+    t, hv, dv = v.shape
+    rep = hv // k.shape[1]
+    q, k = (np.repeat(x / np.sqrt((x * x).sum(-1, keepdims=True) + eps), rep, 1) for x in (q, k))
+    S, out, us = S.copy(), np.zeros((t, hv, dv)), np.zeros((t, hv, dv))
+    old, new = np.zeros((t, hv, dv)), np.zeros((t, hv, dv))
+    for i in range(t):
+        if i % 64 == 0:
+            before, since = np.abs(S), np.zeros((hv, 0))
+        e = np.exp(g[i])
+        before, since = before * e[:, None, None], np.concatenate([since * e[:, None], np.ones((hv, 1))], 1)
+        S = S * e[:, None, None]
+        us[i] = beta[i][:, None] * (v[i] - np.einsum("hkv,hk->hv", S, k[i]))
+        S = S + k[i][:, :, None] * us[i][:, None, :]
+        out[i] = scale * np.einsum("hkv,hk->hv", S, q[i])
+        old[i] = scale * np.einsum("hkv,hk->hv", before, np.abs(q[i]))
+        c = i - i % 64
+        meet = np.abs(np.einsum("hk,jhk->hj", q[i], k[c:i + 1])) * since
+        new[i] = scale * np.einsum("hj,jhv->hv", meet, np.abs(us[c:i + 1]))
+    return out, S, us, old, new
+
+
+def check_tokens(got, got_state, x, lens, dtype, l=64):  # noqa: E741
+    """Every token and head by itself. Terms: the result's rounding; M and U in binary16 (2^-12 each) for a bfloat16
+    result, in 22 bits (2^-21 for both) for a binary16 one; the state and the sums, as state_bound; and the limit that
+    fmoe.h gives: 2^-39 of the largest that a column meets within the chunk, 64 of them in a sum, in each of the right-
+    hand side, U, and T."""
+    q, k, v, g, beta = (ref.f64(t) for t in x[:5])
+    state0, slots, cu = ref.f64(x[5]), x[6].tolist(), x[7].tolist()
+    dk = k.shape[-1]
+    got, got_state, scale = ref.f64(got), ref.f64(got_state), dk ** -0.5
+    eps, operand = torch.finfo(dtype).eps / 2, 2.0 ** (-11 if dtype == torch.bfloat16 else -21)
+    for i, n in enumerate(lens):
+        b = cu[i]
+        out, S, us, old, new = delta_parts(q[b:b + n], k[b:b + n], v[b:b + n], g[b:b + n], beta[b:b + n], state0[slots[i]], scale)
+        for t in range(n):
+            c = t - t % l
+            top = np.maximum(np.abs(us[c:c + l]), np.abs(v[b + c:b + n][:l])).max(0)  # [heads, columns]
+            bound = (eps * np.linalg.norm(out[t], axis=-1) + operand * np.linalg.norm(new[t], axis=-1)
+                     + 4 * state_bound(dk) * (np.linalg.norm(old[t], axis=-1) + np.linalg.norm(new[t], axis=-1))
+                     + scale * 3 * 64 * 2.0 ** -39 * np.linalg.norm(top, axis=-1))
+            off = np.linalg.norm(got[b + t] - out[t], axis=-1)
+            assert (off <= bound).all(), (i, t, (off / bound).max())
+        top = np.abs(us[n - 1 - (n - 1) % l:]).max(0)
+        bound = 2 * state_bound(dk) * np.linalg.norm(S, axis=(1, 2)) + 3 * 64 * 2.0 ** -39 * np.linalg.norm(top, axis=-1)
+        off = np.linalg.norm(got_state[slots[i]] - S, axis=(1, 2))
+        assert (off <= bound).all(), (i, "state", (off / bound).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("large", [False, True])
+def test_delta_chunk_extreme_values_by_token(fmoe, dtype, large):
+    """Zero keys and queries, huge and tiny keys, beta 0 and 1, each token by itself; values 2^20 times the others, in
+    the same chunk (bfloat16)."""
+    lens = [100]
+    x = list(delta_inputs(lens, 2, 2, 64, 64, DT[dtype], 5))
+    q, k, v = (t.clone() for t in x[:3])
+    far = 2.0 ** 40 if dtype == "bf16" else 2.0 ** 10
+    k[3], k[10], k[11], q[7] = 0, k[10] * far, k[11] / far, 0
+    if large:
+        v[30:40] *= 2.0 ** (20 if dtype == "bf16" else 10)
+    x[:3] = q, k, v
+    x[4][::5], x[4][1::5] = 0, 1
+    state = x[5].clone()
+    out = fmoe.delta_chunk(*x[:5], state, x[7], 100, slots=x[6])
+    assert fmoe.sync_status() == 0
+    check_tokens(out, state, x, lens, DT[dtype])
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.02, 3.0])
+def test_delta_chunk_stretches_by_token(fmoe, decay):
+    """Values whose size falls and rises by 2^12 or 2^24; the sequences end in a stretch of small ones."""
+    lens = [700, 520]
+    x = list(delta_inputs(lens, 2, 2, 128, 64, torch.bfloat16, 22, decay=decay))
+    v = x[2].clone()
+    for i, size in enumerate((0, 12, -12, 12, -12)):  # 140 tokens each
+        v[140 * i:140 * (i + 1)] *= 2.0 ** size
+    for i, size in enumerate((12, 0, -12, -12)):  # 130 each
+        v[700 + 130 * i:700 + 130 * (i + 1)] *= 2.0 ** size
+    x[2] = v
+    state = x[5].clone()
+    out = fmoe.delta_chunk(*x[:5], state, x[7], 700, slots=x[6])
+    assert fmoe.sync_status() == 0
+    check_tokens(out, state, x, lens, torch.bfloat16)
+
+
+@pytest.mark.parametrize("lens,dk,dv", [([64], 64, 64), ([300, 77], 128, 128), ([1000], 64, 128)], ids=str)
+def test_delta_chunk_binary16_results(fmoe, lens, dk, dv):
+    """Binary16 results are those of binary32 arithmetic, rounded once."""
+    x = delta_inputs(lens, 2, 4, dk, dv, torch.float16, 30)
+    state = x[5].clone()
+    out = fmoe.delta_chunk(*x[:5], state, x[7], max(lens), slots=x[6])
+    assert fmoe.sync_status() == 0
+    a = [ref.f64(t) for t in x[:6]]
+    want = []
+    for i, n in enumerate(lens):
+        b = int(x[7][i])
+        want.append(ref.delta(*(t[b:b + n] for t in a[:5]), a[5][int(x[6][i])], dk ** -0.5, True, 1e-6)[0])
+    flips(out, np.concatenate(want), torch.float16, state_bound(dk), "out")
+
+
 NAN, INF = float("nan"), float("inf")
 
 
