@@ -30,6 +30,11 @@
 // gates multiply the binary32 results. For a bfloat16 output M, and U where it meets M, are rounded to binary16 (2^-12,
 // its own rounding is 2^-8): they reach nothing but the output. A binary16 output (2^-11) has both parts of M and of
 // U (with M in one its error was 1.4 times the rounding's), and the low parts of S where it meets Q.
+//
+// What is not finite. A product's zeros do not keep a NaN of a later token from the tokens before it, so nothing that is
+// not finite goes into a product of tokens: such a key, query, gate or step size is taken as zeros and its place kept;
+// a right-hand side from its column's first one on too (found by the maximum that is taken anyway). Results from
+// there on, a query's own one, and the column's state are then made NaN.
 #include "api.h"
 #include "mixer.h"
 #include "mma.cuh"
@@ -58,13 +63,15 @@ struct Smem {
   static constexpr int kV = kMl + C * 128, kCa = kV + C * 256, kW = kCa + C * 4, kOut = kW + C * 4, kEnd = kOut + C * 4;
   static constexpr int kStage = (kEnd + 32 + 1023) / 1024 * 1024;
   // behind two stages: rows as they come (32 bytes apart, for the banks), L and in its place the inverse, a product; running
-  // decays with the keys' factors, gates, queries' factors, largest norms and entries, keys' factors with their decay to the end of their 16 tokens, row scales
+  // decays with the keys' factors, gates, queries' factors, largest norms and entries, keys' factors with their decay to the end of their 16 tokens, row scales, first tokens of a row that are not finite
   static constexpr int kRow = DK * 2 + 32, kRaw = 2 * kStage, kL = kRaw + 2 * C * kRow;
   static constexpr int kY = kL + C * LD * 4, kG = kY + 32 * 36 * 4, kBeta = kG + C * 16, kA = kBeta + C * 4;
-  static constexpr int kB = kA + C * 4, kFall = kB + 128, kRows = kFall + C * 4, kBar = kRows + 128 * 8, kBytes = kBar + 64;
+  static constexpr int kB = kA + C * 4, kFall = kB + 128, kRows = kFall + C * 4, kBad = kRows + 128 * 8, kBar = kBad + 128, kBytes = kBar + 64;
 };
 struct Scalars {
-  float decay, t, m, pad;  // e^(G_C); what products with T and with M are multiplied by
+  float decay, t, m;  // e^(G_C); what products with T and with M are multiplied by
+  int first;          // the first token whose key, gate or step size is not finite (C: none)
+  uint32_t odd_q[2];  // a bit for every token whose query is not
 };
 
 // Byte offset of 16-byte chunk q of row r, rows of `row` bytes, chunks permuted by r % 8.
@@ -109,10 +116,11 @@ __device__ __forceinline__ int clamp_exponent(float x) { return max(-100, min(11
 
 // ---------------------------------------------------------------- preparing a chunk (256 threads)
 // Every other 16-byte chunk of row r (keys, then queries) from `raw` to binary16 with the row's exponent taken
-// out. x: the factor that brings products back, 2^e / norm; y: a bound of the norm of what that gives.
+// out. x: the factor that brings products back, 2^e / norm; y: a bound of the norm of what that gives. A row that is not
+// finite becomes zeros and is noted.
 template <typename T, int DK>
 __device__ __forceinline__ float2 prepare_row(const uint8_t* raw, uint8_t* to, int r, int half, bool l2norm, float eps,
-                                              float scale) {
+                                              float scale, Scalars* notes) {
   constexpr int Q = DK / 16;  // 16-byte chunks of half a row
   const uint8_t* const from = raw + r * Smem<DK>::kRow + half * 16;
   uint32_t top = 0u;
@@ -144,6 +152,16 @@ __device__ __forceinline__ float2 prepare_row(const uint8_t* raw, uint8_t* to, i
   }
   float sum = ss[0] + ss[1];
   sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  if (!(sum < INFINITY)) {
+#pragma unroll 1
+    for (int q = half; q < 2 * Q; q += 2)
+      *reinterpret_cast<uint4*>(to + (q >> 3) * Smem<DK>::kPanel + swz(r, q & 7, 128)) = make_uint4(0u, 0u, 0u, 0u);
+    if (r < C)
+      atomicMin(&notes->first, r);
+    else
+      atomicOr(&notes->odd_q[(r - C) >> 5], 1u << (r & 31));
+    return make_float2(0.f, 0.f);
+  }
   // 2^e / sqrt(2^2e ss + eps) = 1 / sqrt(ss + 2^-2e eps), with the two factors of 2^-e apart
   float a = pow2i(e);
   if (l2norm) {
@@ -301,7 +319,7 @@ __device__ __forceinline__ void prepare_chunk(const DeltaRun& r, uint8_t* smem, 
   Scalars* const scalars = reinterpret_cast<Scalars*>(stage + M::kEnd);
   {
     const int row = tid >> 1;
-    const float2 a = prepare_row<T, DK>(smem + M::kRaw, stage + M::kKQ, row, tid & 1, d.l2norm, d.eps, row < C ? 1.0f : d.scale);
+    const float2 a = prepare_row<T, DK>(smem + M::kRaw, stage + M::kKQ, row, tid & 1, d.l2norm, d.eps, row < C ? 1.0f : d.scale, scalars);
     if (!(tid & 1)) *(row < C ? &G[row].z : qb + row - C) = a.x;
     const float top = max_of_warp(a.y);
     if ((tid & 31) == 0) norms[warp] = top;
@@ -507,6 +525,8 @@ __device__ __forceinline__ void prepare_all(const DeltaRun& r, uint8_t* smem, in
     uint8_t* const stage = smem + (n & 1) * M::kStage;
     const int t0 = begin + n * C;
     if (n >= 2) bar_sync(kBarFree + (n & 1), kThreads);
+    Scalars* const notes = reinterpret_cast<Scalars*>(stage + M::kEnd);
+    if (tid == 0) notes->first = C, notes->odd_q[0] = notes->odd_q[1] = 0u;
     copy_wait<0>();  // this chunk's keys and queries
     bar_sync(kBarAux, kAux);
     auto next = [&]() {
@@ -519,6 +539,10 @@ __device__ __forceinline__ void prepare_all(const DeltaRun& r, uint8_t* smem, in
     auto gates = [&]() {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        if (!(gn[j] <= 88.72f && fabsf(bn[j]) < INFINITY)) {  // e^88.73 is infinite
+          gn[j] = bn[j] = 0.f;
+          atomicMin(&notes->first, 2 * lane + j);
+        }
         gn[j] *= kLog2e;
         if (gn[j] < -300.f) gn[j] = -300.f;  // nothing is left below 2^-149
       }
@@ -549,6 +573,12 @@ __device__ __forceinline__ void prepare_all(const DeltaRun& r, uint8_t* smem, in
 }
 
 // ---------------------------------------------------------------- the chain (128 threads, a row each)
+// The larger of two, a NaN where either is one.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 // 32 values times f as the parts of a left operand: 16 columns high, 16 low (where wanted).
 template <bool LOW>
 __device__ __forceinline__ void store_parts(uint32_t to, const uint32_t (&x)[32], float f) {
@@ -681,13 +711,33 @@ __device__ __forceinline__ void chain(const DeltaRun& r, uint8_t* smem, int seq,
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float z = fmaf(-unit * a[i], __uint_as_float(p[j + i]), y[j + i]);
-          mx = fmaxf(mx, fabsf(z));
+          mx = max_or_nan(mx, fabsf(z));
           p[j + i] = __float_as_uint(z);
         }
       }
       tc_store32(lanes + kColP + b, p);
     }
     tc_wait_store();
+    int odd = scalars->first;  // the first token of this row that is not finite
+    if (__any_sync(0xffffffffu, odd < C || !(mx < INFINITY))) {
+      mx = 0.f;
+#pragma unroll 1
+      for (int b = 0; b < C; b += 32) {
+        uint32_t p[32];
+        tc_load32(p, lanes + kColP + b);
+        tc_wait_load();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float z = fabsf(__uint_as_float(p[j]));
+          if (!(z < INFINITY)) odd = min(odd, b + j);
+          if (b + j >= odd) p[j] = 0u;
+          mx = fmaxf(mx, fabsf(__uint_as_float(p[j])));
+        }
+        tc_store32(lanes + kColP + b, p);
+      }
+      tc_wait_store();
+    }
+    smem[M::kBad + row] = (uint8_t)odd;
     int e = clamp_exponent(mx) - kTop;
     const float back = pow2i(e) / unit;
     replace_by_parts(lanes + kColP, pow2i(-e));
@@ -769,6 +819,7 @@ __device__ __forceinline__ void chain(const DeltaRun& r, uint8_t* smem, int seq,
         unit = pow2i(now + shift);
         grow *= f;
       }
+      if (odd < C) grow = NAN;
     }
 #pragma unroll 1
     for (int b = 0; b < C; b += 32) {
@@ -838,7 +889,10 @@ __device__ __forceinline__ void outputs(const DeltaRun& r, uint8_t* smem, int he
     bar_arrive(kBarTaken, 256);
     bar_sync(kBarScales, 256);
     const float2 sc = reinterpret_cast<const float2*>(smem + M::kRows)[row];
-    const float fm = sc.y * reinterpret_cast<const Scalars*>(stage + M::kEnd)->m;
+    const Scalars* const notes = reinterpret_cast<const Scalars*>(stage + M::kEnd);
+    const float fm = sc.y * notes->m;
+    const int odd = smem[M::kBad + row];
+    const uint32_t odd_q[2] = {notes->odd_q[0], notes->odd_q[1]};
     wait_phase(bar, n & 1, r.err);
     tc_fence_after();
 #pragma unroll
@@ -858,6 +912,11 @@ __device__ __forceinline__ void outputs(const DeltaRun& r, uint8_t* smem, int he
         for (int i = 0; i < 4; ++i)
           x[b][j + i] = __float_as_uint(fmaf(a[i] * sc.x, __uint_as_float(x[b][j + i]), fm * __uint_as_float(y[j + i])));
       }
+    }
+    if (odd < C || (odd_q[0] | odd_q[1])) {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (j >= odd || (odd_q[j >> 5] >> (j & 31) & 1u)) x[j >> 5][j & 31] = 0x7fffffffu;  // NaN
     }
     // rows of tokens in the place of the values, which the chain has taken; then out in whole 16 bytes
     {

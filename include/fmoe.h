@@ -361,7 +361,10 @@ int fmoe_delta_step(const fmoe_delta_desc* d, int n, void* stream);
  * what a column of the state meets within 64 tokens (values, and the state's answers to the keys)
  * to 22 bits down to 2^-15 of the largest of them and to 2^-39 of it below: a state that is more
  * than 2^20 times the values and is forgotten within one chunk leaves no exact ones; the
- * recurrent form (max_len 0) does. fresh: nullable [n] bytes; where
+ * recurrent form (max_len 0) does. In both forms a key, gate or step size that is not finite (a
+ * gate: whose exponential is not) leaves its token's results and the later ones of its head, and
+ * the state, not finite; a value, or an entry of the state, those of its column; a query its own
+ * token's; and nothing else. fresh: nullable [n] bytes; where
  * non-zero the sequence starts from a zero state and its slot is only written. */
 int fmoe_delta_chunk(const fmoe_delta_desc* d, const int32_t* cu_seqlens, int n, int n_tokens,
                      int max_len, const uint8_t* fresh, void* stream);

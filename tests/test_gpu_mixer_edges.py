@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import mixer_reference as ref
-from test_gpu_mixers import DT, cache_of, delta_inputs, fmoe, state_bound  # noqa: F401 (fmoe: a fixture)
+from test_gpu_mixers import DT, cache_of, delta_inputs, fmoe, near, state_bound  # noqa: F401 (fmoe: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -131,6 +131,50 @@ def test_delta_chunk_binary16_results(fmoe, lens, dk, dv):
 
 
 NAN, INF = float("nan"), float("inf")
+
+
+ODD = [("k", NAN), ("k", -INF), ("q", NAN), ("q", INF), ("v", NAN), ("v", INF), ("v", -INF), ("g", NAN), ("g", INF),
+       ("beta", NAN), ("beta", INF), ("state", NAN), ("state", -INF)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("what,value", ODD, ids=str)
+@pytest.mark.parametrize("l2norm", [True, False])
+def test_delta_chunk_not_finite(fmoe, dtype, what, value, l2norm):
+    """What is not finite reaches its own token and those behind it (of its column, where it is a value or an entry of
+    the state; its token alone, where it is a query), as in the recurrent form, and nothing else."""
+    lens, dk, dv = [150, 30, 64], 64, 128
+    for at in (0, 20, 63, 64, 149):
+        x = list(delta_inputs(lens, 2, 4, dk, dv, DT[dtype], 40))
+        x = [t.clone() for t in x]
+        if not l2norm:
+            x[0], x[1] = x[0] * 0.09375, x[1] * 0.09375
+        x[1][:, :, 7] = 1 / 16  # no key component that is zero in these columns
+        if what == "state":
+            x[5][x[6][0], 1, 5, 9] = value
+        elif what in "gbeta":
+            x["g beta".split().index(what) + 3][at, 1] = value
+        else:
+            i = "qkv".index(what)
+            x[i][at, 1, 7] = value
+            if what == "q":  # and one in every 16 tokens of the last sequence, and of a short chunk
+                x[0][180::16, 0, 3] = value
+                x[0][155, 0, 3] = value
+        want_state, state = x[5].clone(), x[5].clone()
+        want = fmoe.delta_chunk(*x[:5], want_state, x[7], 0, slots=x[6], l2norm=l2norm)
+        out = fmoe.delta_chunk(*x[:5], state, x[7], 150, slots=x[6], l2norm=l2norm)
+        assert fmoe.sync_status() == 0
+        ok, ok_state = torch.isfinite(want), torch.isfinite(want_state)
+        assert not ok.all()
+        assert torch.equal(torch.isfinite(out), ok), (at, "out")
+        assert torch.equal(torch.isfinite(state), ok_state), (at, "state")
+        # two forms, each within the bound, and two roundings
+        d = DT[dtype]
+        for t in range(0, sum(lens), 10):
+            near(torch.where(ok[t:t + 10], out[t:t + 10], 0), ref.f64(torch.where(ok[t:t + 10], want[t:t + 10], 0)), d,
+                 torch.finfo(d).eps / 2 + 2 ** -11 + 2 * state_bound(dk), f"{at}: out from {t}")
+        near(torch.where(ok_state, state, 0), ref.f64(torch.where(ok_state, want_state, 0)), torch.float32,
+             2 * state_bound(dk), f"{at}: state")
 
 
 # ------------------------------------------------------------------------------------------------ attention
