@@ -43,21 +43,33 @@ __device__ __forceinline__ Place place_of(const fmoe_kv_cache& c, const int32_t*
   return {static_cast<uint8_t*>(c.pages) + (size_t)page * c.heads * block, pos - j * c.page_size};
 }
 
-// Codes of `N` columns of one lane, and the group's scale and bias word.
+// The smaller and the larger of two, a NaN where either is one.
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Codes of `N` columns of one lane, and the group's scale and bias word. A NaN among the 64 makes minimum and maximum
+// NaN in every lane, an infinity the scale infinite: either way all 64 are read back as no numbers.
 template <int N>
 __device__ __forceinline__ uint32_t quantise(const float* x, uint32_t* sb) {
   constexpr int kLanes = 64 / N;  // lanes of a group
   float mn = x[0], mx = x[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) {
-    mn = x[i] < mn ? x[i] : mn;
-    mx = x[i] > mx ? x[i] : mx;
+    mn = min_or_nan(mn, x[i]);
+    mx = max_or_nan(mx, x[i]);
   }
 #pragma unroll
   for (int m = 1; m < kLanes; m <<= 1) {
-    const float a = __shfl_xor_sync(0xffffffffu, mn, m), b = __shfl_xor_sync(0xffffffffu, mx, m);
-    mn = a < mn ? a : mn;
-    mx = b > mx ? b : mx;
+    mn = min_or_nan(mn, __shfl_xor_sync(0xffffffffu, mn, m));
+    mx = max_or_nan(mx, __shfl_xor_sync(0xffffffffu, mx, m));
   }
   // a product, not a division: the nearest bf16 to a fifteenth of the range but where that is within 2^-22 of the
   // middle of two (one group in 400 of binary16 rows is exactly there), and then one of the two all the same

@@ -377,7 +377,9 @@ int fmoe_delta_chunk(const fmoe_delta_desc* d, const int32_t* cu_seqlens, int n,
  *     key sb      [page_size][dim/64 words]  bf16 scale (low half) and bias of 64 columns
  *     value sb    [page_size][dim/64 words]
  * i.e. rows quantised as the qmat rows above: x_hat = q * s + z, by the rule of fmoe_pack with
- * s = bf16((max - min) * (1/15)), both operations and 1/15 rounded to binary32.
+ * s = bf16((max - min) * (1/15)), both operations and 1/15 rounded to binary32. 64 columns with a
+ * NaN or an infinity among them, or with a range beyond binary32, are read back as no finite
+ * numbers, all of them.
  * page_table[i * table_stride + j] is the page of positions j*page_size .. of sequence i. */
 typedef struct fmoe_kv_cache {
     void* pages;       /* 16-byte aligned                                            */

@@ -177,6 +177,32 @@ def test_delta_chunk_not_finite(fmoe, dtype, what, value, l2norm):
              2 * state_bound(dk), f"{at}: state")
 
 
+# ------------------------------------------------------------------------------------------------ the cache
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_append_not_finite(fmoe, dtype, d):
+    """64 columns with a NaN or an infinity among them are read back as no numbers, all of them, wherever it stands;
+    the others are as without it."""
+    ps, n = 16, 64
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.randn(n, 2, d, generator=gen, device="cuda").to(DT[dtype])
+    odd = x.clone()
+    for t in range(n):
+        odd[t, t % 2, (t * 5) % d] = (NAN, INF, -INF)[t % 3]
+    P, S = torch.arange(n, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    table = torch.arange(n // ps, dtype=torch.int32, device="cuda")[None]
+    held = []
+    for rows in (x, odd):
+        pages = fmoe.kv_pages(n // ps, 2, d, ps)
+        fmoe.kv_append(rows, rows, P, pages, table, torch.zeros(0, device="cuda"), seq=S)
+        held.append(fmoe.kv_read(pages, table, P, d, seq=S, dtype=torch.float32))
+    assert fmoe.sync_status() == 0
+    hit = ~torch.isfinite(odd.float()).view(n, 2, d // 64, 64).all(-1, keepdim=True).expand(n, 2, d // 64, 64).reshape(n, 2, d)
+    for clean, got in zip(*held):
+        assert not torch.isfinite(got[hit]).any()
+        assert torch.equal(got[~hit], clean[~hit])
+
+
 # ------------------------------------------------------------------------------------------------ attention
 def unpacked(pages, ps, d):
     """Pages of one kv head [pages, bytes] on the GPU -> keys, values [positions, d] in binary64."""
