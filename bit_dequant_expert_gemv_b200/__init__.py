@@ -376,6 +376,21 @@ def _device(t):
     return dev
 
 
+def _empty(like, shape, dtype, stream):
+    """Memory for a result that `stream` writes, on the device of `like`. Free memory of the current stream may still be
+    written by what that stream has yet to run: another stream's result is allocated on that one, and outlives the
+    current one's use of it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=like.device)
+    out.record_stream(torch.cuda.current_stream(like.device))
+    return out
+
+
 def _call(fn, dev, stream, *args):
     """fn(*args, stream) with the tensors' device current; the stream is that device's current one by default."""
     import torch
@@ -392,7 +407,7 @@ def _call(fn, dev, stream, *args):
         _ck(fn, rc)
 
 
-def _delta(dev, q, k, v, g, beta, state, n, slots, scale, l2norm, eps, out):
+def _delta(dev, q, k, v, g, beta, state, n, slots, scale, l2norm, eps, out, stream):
     import torch
     dt = v.dtype
     code = _dtype(dt)
@@ -416,7 +431,7 @@ def _delta(dev, q, k, v, g, beta, state, n, slots, scale, l2norm, eps, out):
         raise ValueError("state must be float32 [slots, heads, dim_k, dim_v], contiguous within a slot")
     sp = _array(slots, torch.int32, dev, "slots", n)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=v.device)
+        out = _empty(v, shape, dt, stream)
     ov = _rows(out, dt, dev, "out", shape)
     return out, DeltaDesc(heads_k, heads_v, dim_k, dim_v, code, l2norm, eps,
                           dim_k ** -0.5 if scale is None else scale, *qv, *kv, *vv, g.data_ptr(),
@@ -428,7 +443,7 @@ def delta_step(q, k, v, g, beta, state, slots=None, scale=None, l2norm: bool = T
                eps: float = 1e-6, out=None, stream=None):
     """One token of every sequence through the gated delta rule; `state` is updated in place."""
     dev, n = _device(v), v.shape[0]
-    out, d = _delta(dev, q, k, v, g, beta, state, n, slots, scale, l2norm, eps, out)
+    out, d = _delta(dev, q, k, v, g, beta, state, n, slots, scale, l2norm, eps, out, stream)
     _call("fmoe_delta_step", dev, stream, d, n)
     return out
 
@@ -438,7 +453,7 @@ def delta_chunk(q, k, v, g, beta, state, cu_seqlens, max_len: int, slots=None, f
     """Packed sequences (prompts) through the gated delta rule; `state` is updated in place."""
     import torch
     dev, n = _device(v), cu_seqlens.numel() - 1
-    out, d = _delta(dev, q, k, v, g, beta, state, n, slots, scale, l2norm, eps, out)
+    out, d = _delta(dev, q, k, v, g, beta, state, n, slots, scale, l2norm, eps, out, stream)
     cu = _array(cu_seqlens, torch.int32, dev, "cu_seqlens", n + 1)
     if fresh is not None and fresh.dtype is torch.bool:
         fresh = fresh.view(torch.uint8)
@@ -501,7 +516,7 @@ def kv_append(k, v, positions, pages, page_table, inv_freq, seq=None, q=None, q_
         if q_shape != (tokens, heads_q, dim):
             raise ValueError(f"q has shape {tuple(q_shape)}, expected ({tokens}, heads, {dim})")
         if q_out is None:
-            q_out = torch.empty(q_shape, dtype=dt, device=k.device)
+            q_out = _empty(k, q_shape, dt, stream)
         ov = _rows(q_out, dt, dev, "q_out", q_shape)
     a = KvTokens(code, tokens, *kv, *vv, pp, sp, fp, n_freq, interleaved, heads_q, *qv, *ov)
     _call("fmoe_kv_append", dev, stream, c, a)
@@ -517,8 +532,8 @@ def kv_read(pages, page_table, positions, dim: int, seq=None, dtype=None, k=None
     tokens = positions.numel()
     shape = (tokens, c.heads, dim)
     dt = dtype if dtype is not None else torch.bfloat16 if k is None else k.dtype
-    k = torch.empty(shape, dtype=dt, device=pages.device) if k is None else k
-    v = torch.empty(shape, dtype=dt, device=pages.device) if v is None else v
+    k = _empty(pages, shape, dt, stream) if k is None else k
+    v = _empty(pages, shape, dt, stream) if v is None else v
     pp = _array(positions, torch.int32, dev, "positions", tokens)
     sp = _array(seq, torch.int32, dev, "seq", tokens)
     _call("fmoe_kv_read", dev, stream, c, pp, sp, tokens, _dtype(dt), View(*_rows(k, dt, dev, "k", shape)),
@@ -536,7 +551,7 @@ def attn_q4(q, pages, page_table, lens, max_len: int, cu_q=None, max_q: int = 1,
     qv = _rows(q, dt, dev, "q")
     tokens, heads, dim = shape = q.shape
     c = _cache(dev, pages, page_table, dim)
-    out = torch.empty(shape, dtype=dt, device=q.device) if out is None else out
+    out = _empty(q, shape, dt, stream) if out is None else out
     ov = _rows(out, dt, dev, "out", shape)
     lp = _array(lens, torch.int32, dev, "lens", c.n_seqs)
     cp = _array(cu_q, torch.int32, dev, "cu_q", c.n_seqs + 1)

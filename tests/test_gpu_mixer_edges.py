@@ -367,3 +367,38 @@ def test_attention_from_two_threads(fmoe):
     torch.cuda.synchronize()
     for _, want, out, *_ in calls:
         assert torch.equal(out, want)
+
+
+def test_results_on_another_stream(fmoe):
+    """A result that a call makes for itself on the stream it is given is not memory that the current stream still
+    writes."""
+    n, hv, d, ps = 64, 8, 64, 16
+    x = delta_inputs([1] * n, 4, hv, d, d, torch.bfloat16, 3)
+    pages, table = cache_of([20] * n, 4, d, ps, 8)
+    L = torch.full((n,), 20, dtype=torch.int32, device="cuda")
+    q = torch.randn(n, hv, d, device="cuda").to(torch.bfloat16)
+    P, inv = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.ones(8, device="cuda")
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    k = torch.randn(n, 4, d, device="cuda").to(torch.bfloat16)
+    state = x[5].clone()
+    calls = [lambda s: fmoe.delta_step(*x[:5], state, slots=x[6], stream=s),
+             lambda s: fmoe.delta_chunk(*x[:5], state, cu, 1, slots=x[6], stream=s),
+             lambda s: fmoe.attn_q4(q, pages, table, L, 20, stream=s),
+             lambda s: fmoe.kv_append(k, k, P, pages, table, inv, q=q, stream=s)]
+    st = torch.cuda.Stream()
+    for call in calls:
+        state.copy_(x[5])
+        want = call(None).clone()
+        for s in (st, st.cuda_stream):
+            state.copy_(x[5])
+            torch.cuda.synchronize()
+            held = torch.empty(n, hv, d, dtype=torch.bfloat16, device="cuda")
+            at = held.data_ptr()
+            torch.cuda._sleep(20_000_000)  # about 10 ms, and then a write, of which the allocator knows by the stream's order
+            held.fill_(7)
+            del held
+            out = call(s)
+            assert out.data_ptr() != at
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+    assert fmoe.sync_status() == 0
