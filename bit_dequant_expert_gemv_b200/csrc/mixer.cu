@@ -25,10 +25,23 @@ int check_view(const char* name, const void* p, int64_t token_stride, int64_t he
   return FMOE_OK;
 }
 
+// Whether two of the rows [token][head] of `dim` elements share an element.
+bool rows_overlap(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride, int64_t head_stride) {
+  if ((tokens > 1 && token_stride < dim) || (heads > 1 && head_stride < dim)) return true;
+  if (tokens < 2 || heads < 2) return false;
+  const __int128 ts = token_stride, hs = head_stride;
+  if (ts >= (heads - 1) * hs + dim || hs >= (tokens - 1) * ts + dim) return false;  // one inside the other: the usual
+  for (int64_t h = 1; h < heads; ++h) {  // strides that interleave: the tokens on either side of a head's offset
+    const __int128 t = h * hs / ts, off = h * hs - t * ts;
+    if ((t < tokens && off < dim) || (t + 1 < tokens && ts - off < dim)) return true;
+  }
+  return false;
+}
+
 int check_out(const char* name, const fmoe_out_view& v, int heads, int dim, int tokens, int dtype) {
   const int rc = check_view(name, v.ptr, v.token_stride, v.head_stride, dtype);
   if (rc) return rc;
-  if ((heads > 1 && v.head_stride < dim) || (tokens > 1 && v.token_stride < dim))
+  if (rows_overlap(tokens, heads, dim, v.token_stride, v.head_stride))
     return fail(FMOE_ERR_INVALID, "%s has overlapping rows", name);
   return FMOE_OK;
 }
