@@ -2,6 +2,8 @@
 // and launches (kernels in delta.cu, delta_chunk.cu, kv.cu, attn.cu).
 #include "mixer.h"
 
+#include <cmath>
+
 #include "api.h"
 
 using namespace fmoe;
@@ -186,6 +188,7 @@ int fmoe_attn_q4(const fmoe_kv_cache* cache, const fmoe_attn_desc* a, void* stre
     return fail(FMOE_ERR_INVALID, "heads_q (%d) must be a positive multiple of the cache's heads (%d)", a->heads_q,
                 cache->heads);
   if (a->n_tokens < 0 || a->max_q < 0 || a->max_len < 0) return fail(FMOE_ERR_INVALID, "negative count");
+  if (!std::isfinite(a->scale)) return fail(FMOE_ERR_INVALID, "scale is not finite");
   if (!a->cu_q && a->n_tokens != cache->n_seqs)
     return fail(FMOE_ERR_INVALID, "%d queries for %d sequences without cu_q", a->n_tokens, cache->n_seqs);
   if (a->n_tokens == 0 || cache->n_seqs == 0) return FMOE_OK;

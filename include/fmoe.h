@@ -440,7 +440,7 @@ typedef struct fmoe_attn_desc {
     int dtype;               /* of q, out                                             */
     int n_tokens;            /* query rows                                            */
     int max_q, max_len;
-    float scale;
+    float scale;             /* finite                                                */
     fmoe_view q;             /* [n_tokens][heads_q][dim]                              */
     const int32_t* cu_q;     /* nullable [n_seqs+1]                                   */
     const int32_t* lens;     /* [n_seqs]                                              */

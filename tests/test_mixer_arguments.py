@@ -43,3 +43,11 @@ def test_overlapping_results_of_every_call():
     assert L.fmoe_attn_q4(cache, attn, None) == fmoe.FMOE_ERR_INVALID and "overlapping" in fmoe.last_error()
     tokens = fmoe.KvTokens(fmoe.FMOE_BF16, 2, P, 512, 128, P, 512, 128, P, None, P, 64, 0, 2, P, 512, 128, P, 128, 128)
     assert L.fmoe_kv_append(cache, tokens, None) == fmoe.FMOE_ERR_INVALID and "overlapping" in fmoe.last_error()
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_attention_scale_that_is_not_finite(scale):
+    """Logits times no number are no weights: a NaN would come out as like weights for all positions."""
+    cache = fmoe.KvCacheDesc(P, 10, 2, 128, 64, P, 4, 2, 4)
+    attn = fmoe.AttnDesc(2, fmoe.FMOE_BF16, 2, 1, 256, scale, P, 512, 128, None, P, P, 512, 128)
+    assert fmoe.lib().fmoe_attn_q4(cache, attn, None) == fmoe.FMOE_ERR_INVALID and "scale" in fmoe.last_error()
