@@ -175,7 +175,8 @@ __device__ __forceinline__ float bias_of(uint32_t sb) { return __uint_as_float(s
 // p s / 2^E is held in binary16 times 2^kLift. The running maximum follows the scores' only when they pass it
 // by kSlack (base 2), and E is set one above a scale's exponent: most stages then leave the sums as they are. A
 // scale is below 2^(E + 1), so p s stays below 2^(kLift + kSlack + 1) = 2^15, and it is a normal number down to
-// 2^-23 of the largest scale.
+// 2^-22 of 2^E; below that it is held to 2^-33 of 2^E, 2^-32 of the largest scale. The exponent goes by the scales and not by
+// p s: that would take another maximum of every row, three shuffles a row and stage.
 constexpr int kLift = 8, kSlack = 6;
 constexpr int kMinE = kLift;
 constexpr int kShort = 8;  // stages of a ring that are not worth sharing

@@ -427,7 +427,10 @@ int fmoe_kv_read(const fmoe_kv_cache* cache, const int32_t* positions, const int
  * cu_q[i] .. cu_q[i+1]-1 (NULL: query i alone), which are its last positions: the j-th of n_i
  * queries sees positions 0 .. lens[i] - n_i + j. Query head h reads kv head h / (heads_q / heads).
  *     out = sum_t p_t v_hat_t,  p = softmax(scale * q . k_hat_t)   over the positions seen
- * A query that sees nothing gives zeros. Softmax statistics and sums are binary32.
+ * A query that sees nothing gives zeros. Softmax statistics and sums are binary32. A position's
+ * p times the scale of its values goes into them to 2^-12 of itself for FMOE_BF16, to 2^-22 else, and
+ * to 2^-32 of the largest scale of the values seen: of positions whose scales are 2^-20 of another's,
+ * little is left beside it, whatever the weights.
  * What no query sees may hold anything. A key's scale or bias that is seen and not finite makes the
  * query's results so, a value's those of its 64 columns (all of the query's, where another query of
  * its sequence does not see that position).

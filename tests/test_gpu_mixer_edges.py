@@ -276,6 +276,41 @@ def test_attention_long_as_a_whole(fmoe, scale):
 
 
 @pytest.mark.parametrize("dtype", list(DT))
+def test_attention_small_scales_that_decide(fmoe, dtype):
+    """Positions of large value scales and next to no weight beside positions of scales 2^-10 of theirs and all the
+    weight. The product of weight and scale is held to 2^-12 of itself (bfloat16) or 2^-22, and to 2^-32 of the largest
+    scale (fmoe.h), times codes of 16 at most; the rest as check_attn has it."""
+    n, d, ps, dt, scale = 200, 64, 16, DT[dtype], 0.25
+    pages, table = cache_of([n], 1, d, ps, 61)
+    sb = pages[:, :, ps * d:].view(torch.bfloat16).view(-1, 1, 2, ps, 1, 2)
+    for t in range(n):
+        page, at = int(table[0, t // ps]), t % ps
+        if t % 5 == 2:
+            sb[page, 0, 0, at] = torch.tensor([0.0, -4.0], device="cuda").to(torch.bfloat16)  # -4 in all columns: a logit of -64
+        else:
+            sb[page, 0, 1, at] *= 2.0 ** -10
+            sb[page, 0, 0, at] *= 2.0 ** -4
+    q = (0.5 + torch.rand(1, 8, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))).to(dt)
+    out = fmoe.attn_q4(q, pages, table, torch.tensor([n], dtype=torch.int32, device="cuda"), n, scale=scale)
+    assert fmoe.sync_status() == 0
+    mine = pages[:, 0][table[0].long()]
+    k, v = (x[:n] for x in unpacked(mine, ps, d))
+    sb = mine[:, ps * d:].contiguous().view(torch.bfloat16).view(-1, 2, ps, 2).double()
+    sk, sv, zv = sb[:, 0, :, 0].reshape(-1)[:n], sb[:, 1, :, 0].reshape(-1)[:n], sb[:, 1, :, 1].reshape(-1)[:n]
+    for r in range(8):
+        x = scale * (k @ q[0, r].double())
+        p = torch.softmax(x, -1)
+        want = p @ v
+        mass = scale * (k.abs() + 16 * sk[:, None]) @ q[0, r].double().abs()
+        dx = 2 * (d + 8) * 2.0 ** -24 * float(mass.max()) + 2.0 ** -22 * (1 + float(x.abs().max()))
+        codes = float(p @ (15 * sv + zv.abs()))
+        bound = (torch.finfo(dt).eps / 2 * want.abs() + (2.0 ** (-12 if dtype == "bf16" else -21) + 2 * dx) * codes
+                 + 2.0 ** -32 * n * 16 * float(sv.max()))
+        off = (out[0, r].double() - want).abs()
+        assert bool((off <= bound).all()), (r, float((off / bound).max()))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("value", [NAN, INF, -INF])
 def test_attention_values_not_finite(fmoe, dtype, value):
     """A value scale or bias that is not finite makes its 64 columns so, and no others."""
