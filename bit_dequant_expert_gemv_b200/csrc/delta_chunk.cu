@@ -191,33 +191,21 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return make_float2(hi, __fsub_rn(e, __fsub_rn(hi, s)));
 }
 
-// For R rows and N columns: sum over k < K of a[r][k] b[k][..]; a's rows `lda[r]`, columns of b at ldb.
-template <int K, int R, int N>
-__device__ __forceinline__ void small_product(float (&s)[R][N], const float* const (&a)[R], const float* b, int ldb) {
+// Two columns of a row of a product over 8: the sum of a[k] b[k][0..1], b's rows ldb apart.
+__device__ __forceinline__ float2 row_product(const float* a, const float* b, int ldb) {
+  float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int k = 0; k < K; k += 4) {
-    float x[R][4];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float4 v = *reinterpret_cast<const float4*>(a[r] + k);
-      x[r][0] = v.x, x[r][1] = v.y, x[r][2] = v.z, x[r][3] = v.w;
-    }
+  for (int k = 0; k < 8; k += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(a + k);
+    const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float y[N];
-      if constexpr (N == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(b + (k + j) * ldb);
-        y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(b + (k + j) * ldb);
-        y[0] = v.x, y[1] = v.y;
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int n = 0; n < N; ++n) s[r][n] = fmaf(x[r][j], y[n], s[r][n]);
+      const float2 y = *reinterpret_cast<const float2*>(b + (k + j) * ldb);
+      s.x = fmaf(x[j], y.x, s.x);
+      s.y = fmaf(x[j], y.y, s.y);
     }
   }
+  return s;
 }
 
 // One 16 x 8 tile of a product over K, by a warp, in tf32 parts (the products of two low parts are left out:
@@ -269,16 +257,11 @@ __device__ __forceinline__ void invert(float* X, float* Y, int tid) {
     __syncwarp();
     const int o = 16 * warp, row = lane >> 2, col = 2 * (lane & 3);
     float* const y = Y + warp * 8 * 12;
-    float s[1][2] = {};
-    const float* const a[1] = {X + (o + 8 + row) * LD + o};
-    small_product<8>(s, a, X + o * LD + o + col, LD);
-    *reinterpret_cast<float2*>(y + row * 12 + col) = make_float2(s[0][0], s[0][1]);
+    *reinterpret_cast<float2*>(y + row * 12 + col) = row_product(X + (o + 8 + row) * LD + o, X + o * LD + o + col, LD);
     *reinterpret_cast<float2*>(X + (o + row) * LD + o + 8 + col) = make_float2(0.f, 0.f);
     __syncwarp();
-    float t[1][2] = {};
-    const float* const d[1] = {X + (o + 8 + row) * LD + o + 8};
-    small_product<8>(t, d, y + col, 12);
-    *reinterpret_cast<float2*>(X + (o + 8 + row) * LD + o + col) = make_float2(-t[0][0], -t[0][1]);
+    const float2 t = row_product(X + (o + 8 + row) * LD + o + 8, y + col, 12);
+    *reinterpret_cast<float2*>(X + (o + 8 + row) * LD + o + col) = make_float2(-t.x, -t.y);
   }
   bar_sync(kBarAux, kAux);
   {  // 16 and 16: a pair of blocks by two warps; the others clear what lies above them

@@ -47,21 +47,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return d;
 }
 
-// Four 8 x 8 matrices of 16-bit values from shared memory; lane l gives the address of row l % 8 of
-// matrix l / 8 (16 bytes). Thread: row g, columns 2c, 2c+1 of each; transposed: column g, rows 2c, 2c+1.
-__device__ __forceinline__ void load_matrices(uint32_t (&d)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void load_matrices_t(uint32_t (&d)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-               : "r"(addr)
-               : "memory");
-}
-
 // Asynchronous 16-byte copies from global to shared memory.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
