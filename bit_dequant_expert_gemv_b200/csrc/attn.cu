@@ -63,15 +63,11 @@ __device__ __forceinline__ Seq seq_of(const AttnRun& r, int i, bool tell) {
   s.q0 = r.a.cu_q ? r.a.cu_q[i] : i;
   const int q1 = r.a.cu_q ? r.a.cu_q[i + 1] : i + 1;
   s.len = r.a.lens[i];
-  s.nq = q1 - s.q0;
+  const bool queries = s.q0 >= 0 && q1 >= s.q0 && q1 <= r.a.n_tokens;  // compared, not subtracted: any numbers may stand there
+  s.nq = queries ? q1 - s.q0 : 0;
   const long long room = (long long)r.c.max_pages * r.c.page_size;
   s.limit = (int)min((long long)min(max(s.len, 0), r.a.max_len), room);
-  bool bad = s.len != s.limit || s.nq > r.a.max_q;
-  if (s.q0 < 0 || s.nq < 0 || q1 > r.a.n_tokens) {
-    bad = true;
-    s.nq = 0;
-  }
-  if (bad && tell) report(r.err, ERR_LENGTH);
+  if (tell && (!queries || s.len != s.limit || s.nq > r.a.max_q)) report(r.err, ERR_LENGTH);
   return s;
 }
 // Positions seen by query j of a sequence.
@@ -84,8 +80,7 @@ constexpr int kStages = 2;  // of a ring: three gained nothing at any of the siz
 
 // Passes of a sequence: none without queries, else at least one (a query that sees nothing gives zeros).
 __device__ __forceinline__ int passes_of(const AttnRun& r, int i) {
-  const int nq = r.a.cu_q ? r.a.cu_q[i + 1] - r.a.cu_q[i] : 1;
-  if (nq <= 0) return 0;
+  if (r.a.cu_q && r.a.cu_q[i + 1] <= r.a.cu_q[i]) return 0;
   const long long room = (long long)r.c.max_pages * r.c.page_size;
   const int len = (int)min((long long)min(max(r.a.lens[i], 0), r.a.max_len), room);
   return max(1, (len + kStage - 1) / kStage);

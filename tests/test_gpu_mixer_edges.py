@@ -352,6 +352,21 @@ def test_attention_counts_that_fall_back(fmoe, most):
     assert fmoe.sync_status() == 0
 
 
+@pytest.mark.parametrize("most", [100, 9000])
+def test_attention_counts_of_any_numbers(fmoe, most):
+    """Whatever stands in cu_q: rows outside 0 .. n_tokens are not touched, and it is reported."""
+    lens, d, ps = [100, 60], 64, 16
+    pages, table = cache_of([most, 60], 1, d, ps, 4)
+    wide = torch.randn(72, 2, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    out = torch.full_like(wide, 7.0)
+    L = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    low, high = -2 ** 31, 2 ** 31 - 1
+    for cu in ([0, 5, low], [5, low, 8], [0, 5, -3], [low, 5, 8], [0, high, 8], [8, high, low], [low, high, 8], [7, 8, high]):
+        fmoe.attn_q4(wide[32:40], pages, table, L, most, cu_q=torch.tensor(cu, dtype=torch.int32, device="cuda"), max_q=32, out=out[32:40])
+        assert fmoe.sync_status() == fmoe.FMOE_ERR_INDEX and "length" in fmoe.last_error(), cu
+        assert (out[:32] == 7).all() and (out[40:] == 7).all(), cu
+
+
 def test_attention_of_2_31_passes(fmoe):
     """More than 2^31 passes: a table that names one page again and again, and a bound of the queries that gives 65520
     blocks of rows, all empty but one. The result is that of the one page, but for sums of up to 2^17 terms in a row:
