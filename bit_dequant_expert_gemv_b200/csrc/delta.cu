@@ -122,8 +122,9 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent(const DeltaRun r) {
       kq += dots[buf][w][2];
     }
     const float eg = expf(g);
-    const float kappa = d.l2norm ? 1.0f / sqrtf(kk + d.eps) : 1.0f;
-    const float rho = d.scale * (d.l2norm ? 1.0f / sqrtf(qq + d.eps) : 1.0f);
+    // a row of zeros stays one where eps is zero too (a NaN takes the first branch)
+    const float kappa = d.l2norm ? (kk + d.eps != 0.f ? 1.0f / sqrtf(kk + d.eps) : 0.f) : 1.0f;
+    const float rho = d.scale * (d.l2norm ? (qq + d.eps != 0.f ? 1.0f / sqrtf(qq + d.eps) : 0.f) : 1.0f);
     const float decay = eg * kappa, own = kappa * kq;
     float u[4];
 #pragma unroll

@@ -327,7 +327,8 @@ typedef struct fmoe_out_view {
 
 /* The gated delta rule. Per value head h (key head h / (heads_v / heads_k)) with a state S of
  * dim_k x dim_v, for each token of a sequence in order:
- *     k~ = k / sqrt(sum k^2 + eps), q~ = q / sqrt(sum q^2 + eps)   (l2norm; else k~ = k, q~ = q)
+ *     k~ = k / sqrt(sum k^2 + eps), q~ = q / sqrt(sum q^2 + eps)   (l2norm; else k~ = k, q~ = q;
+ *     a row of zeros stays one with eps = 0)
  *     S' = exp(g) S;  u = beta (v - S'^T k~);  S = S' + k~ u^T;  out = scale S^T q~
  * g is a log decay (<= 0 in use), beta a step size. States and every sum are binary32. */
 typedef struct fmoe_delta_desc {

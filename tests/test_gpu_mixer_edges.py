@@ -177,6 +177,31 @@ def test_delta_chunk_not_finite(fmoe, dtype, what, value, l2norm):
              2 * state_bound(dk), f"{at}: state")
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+def test_delta_rows_of_zeros_without_eps(fmoe, dtype):
+    """Keys and queries of zeros stay zeros where they are divided by a norm of zero, in every form."""
+    lens, dk, dv = [40, 17], 64, 64
+    x = [t.clone() for t in delta_inputs(lens, 2, 2, dk, dv, DT[dtype], 44)]
+    x[1][5], x[0][9], x[1][45, 1] = 0, 0, 0
+    a = [ref.f64(t) for t in x[:6]]
+    a[0], a[1] = (t / np.maximum(np.linalg.norm(t, axis=-1, keepdims=True), 1e-30) for t in a[:2])
+    for most in (0, 40):
+        state = x[5].clone()
+        out = fmoe.delta_chunk(*x[:5], state, x[7], most, slots=x[6], eps=0.0)
+        assert fmoe.sync_status() == 0
+        for i, n in enumerate(lens):
+            b, slot = int(x[7][i]), int(x[6][i])
+            o, S = ref.delta(*(t[b:b + n] for t in a[:5]), a[5][slot], dk ** -0.5, False, 0.0)
+            near(out[b:b + n], o, DT[dtype], 2 ** -11 * (dtype == "bf16") + state_bound(dk), (most, "out"))
+            near(state[slot], S, torch.float32, state_bound(dk), (most, "state"))
+    one = [t[5:6].contiguous() for t in x[:5]]
+    state = x[5].clone()
+    out = fmoe.delta_step(*one, state, slots=x[6][:1], eps=0.0)
+    o, S = ref.delta(*(t[5:6] for t in a[:5]), a[5][int(x[6][0])], dk ** -0.5, False, 0.0)
+    near(out, o, DT[dtype], state_bound(dk), "step")
+    near(state[x[6][0]], S, torch.float32, state_bound(dk), "step's state")
+
+
 # ------------------------------------------------------------------------------------------------ the cache
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("d", [64, 128, 256])
