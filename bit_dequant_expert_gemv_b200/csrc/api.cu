@@ -347,7 +347,7 @@ extern "C" {
 
 const char* fmoe_last_error(void) { return g_err.c_str(); }
 
-int fmoe_version(void) { return 10000; }
+int fmoe_version(void) { return 10100; }
 
 void fmoe_set_wait_budget_ns(uint64_t ns) { g_wait_ns = ns < 1000 ? 1000 : ns; }
 

@@ -51,3 +51,7 @@ def test_attention_scale_that_is_not_finite(scale):
     cache = fmoe.KvCacheDesc(P, 10, 2, 128, 64, P, 4, 2, 4)
     attn = fmoe.AttnDesc(2, fmoe.FMOE_BF16, 2, 1, 256, scale, P, 512, 128, None, P, P, 512, 128)
     assert fmoe.lib().fmoe_attn_q4(cache, attn, None) == fmoe.FMOE_ERR_INVALID and "scale" in fmoe.last_error()
+
+
+def test_version_has_the_token_mixers():
+    assert fmoe.lib().fmoe_version() >= 10100
