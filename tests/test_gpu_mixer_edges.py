@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import mixer_reference as ref
-from test_gpu_mixers import DT, cache_of, delta_inputs, fmoe, near, state_bound  # noqa: F401 (fmoe: a fixture)
+from test_gpu_mixers import DT, cache_of, delta_inputs, fmoe, near, paged, state_bound  # noqa: F401 (fmoe: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -476,4 +476,40 @@ def test_results_on_another_stream(fmoe):
             assert out.data_ptr() != at
             torch.cuda.synchronize()
             assert torch.equal(out, want)
+    assert fmoe.sync_status() == 0
+
+
+def test_prompts_captured_and_replayed(fmoe):
+    """A prompt's calls in one graph, replayed on other inputs, lengths, positions and slots: what eager calls give."""
+    lens, others, d, ps = [70, 33], [21, 82], 128, 16
+    sets = []
+    for seed, ls in ((1, lens), (2, others)):
+        x = delta_inputs(ls, 2, 4, d, d, torch.bfloat16, seed)
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        kv = torch.randn(103, 12, d, generator=gen, device="cuda").to(torch.bfloat16)
+        pos = torch.cat([torch.arange(n) for n in ls]).to("cuda", torch.int32)
+        seq = torch.repeat_interleave(torch.arange(2), torch.tensor(ls)).to("cuda", torch.int32)
+        sets.append([*(t.contiguous() for t in x), kv, pos, seq, torch.tensor(ls, dtype=torch.int32, device="cuda")])
+    inv = torch.rand(32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    table, n_pages = paged(2, 96, ps, 5)
+
+    def calls(q, k, v, g, beta, state, slots, cu, kv, pos, seq, L, pages):
+        o = fmoe.delta_chunk(q, k, v, g, beta, state, cu, 96, slots=slots)
+        turned = fmoe.kv_append(kv[:, 8:10], kv[:, 10:], pos, pages, table, inv, seq=seq, q=kv[:, :8])
+        a = fmoe.attn_q4(turned, pages, table, L, 96, cu_q=cu, max_q=96)
+        return [o, turned, a, *fmoe.kv_read(pages, table, pos, d, seq=seq), state, pages]
+    want = [[t.clone() for t in calls(*(t.clone() for t in s), fmoe.kv_pages(n_pages, 2, d, ps))] for s in sets]
+    held, pages = [t.clone() for t in sets[0]], fmoe.kv_pages(n_pages, 2, d, ps)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(*held, pages)
+    for i in (1, 0, 1):
+        for a, b in zip(held, sets[i]):
+            a.copy_(b)
+        pages.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want[i]):
+            assert torch.equal(a, b)
     assert fmoe.sync_status() == 0
