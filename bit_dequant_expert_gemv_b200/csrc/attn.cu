@@ -23,15 +23,18 @@
 //
 // Work is cut in passes of 32 positions per warp. All passes of all (sequence, kv head, block of rows)
 // items stand in one row, and every CTA takes an equal share of it, wherever items begin and end:
-// lengths of any mixture keep every SM busy to the end. What a CTA has of an item that others share goes
-// to scratch (at most its first and its last item), and a second launch joins the parts, in order.
+// lengths of any mixture keep every SM busy to the end. (Of sequences with like numbers of queries: every sequence
+// counts the blocks of rows that max_q gives, and the CTAs that get empty ones are done at once. A long prompt among
+// single queries runs on the few CTAs that its share of the positions gives it.) What a CTA has of an item that others
+// share goes to scratch (at most its first and its last item), and a second launch joins the parts, in order.
 //
-// Measured, bf16, 32 query heads: 32 requests of up to 8192 positions, 4 kv heads of 128: 44 us; one of 262144, 2
-// of 256: 71 us, of which 23 us would be the codes' bytes at the copy rate. Instructions bound it, and that each
-// waits for the one before: unpacking, scales and softmax take 27.8 million warp instructions for the long one
-// (whatever the number of query rows below eight), issued in 43 % of the cycles by the two warps of a scheduler
-// whose registers the sums leave room for (54 % by the four warps at 128 columns). One request of 777 positions:
-// 14 us, seven stages of 32 one after another.
+// Measured, 32 query heads: 32 requests of up to 8192 positions, 4 kv heads of 128: 44 us for bfloat16, 53 for binary16,
+// 58 for binary32; one of 262144, 2 of 256: 73, 97 and 119 us, of which 23 us would be the codes' bytes at the copy
+// rate. Instructions bound it, and that each waits for the one before: unpacking, scales and softmax take 29.9 million
+// warp instructions for the long one in bfloat16, issued in 44 % of the cycles by the two warps of a scheduler whose
+// registers the sums leave room for (54 % by the four warps at 128 columns). At 256 columns and 16 rows 255 registers
+// do not hold them all: 240 bytes are stored and 252 loaded again. One request of 777 positions: 14 us, seven stages of
+// 32 one after another.
 #include "api.h"
 #include "mixer.h"
 #include "mma.cuh"
@@ -174,14 +177,18 @@ __device__ __forceinline__ float bias_of(uint32_t sb) { return __uint_as_float(s
 // p s: that would take another maximum of every row, three shuffles a row and stage.
 constexpr int kLift = 8, kSlack = 6;
 constexpr int kMinE = kLift;
-constexpr int kShort = 8;  // stages of a ring that are not worth sharing
+// Stages of a ring that are not worth sharing (1024 positions). An item whole and shared, us: 4 items of 256, 777 and 1024
+// positions 8.5 and 11.6, 14.4 and 15.8, 15.7 and 16.4; 128 items 8.9 and 20.5, 13.7 and 23.1, 15.7 and 23.4. One item
+// alone (a request with one kv head) is better shared from 777 positions on: 14.3 and 11.2, 15.7 and 11.6.
+constexpr int kShort = 8;
 
 // How the operands of the two products are held for results of type T, beside sums of binary32.
 //   q: binary16 parts of a query. One holds a 16-bit query as it is, two a binary32 one (22 bits).
 //   ps: binary16 parts of p s. One (2^-12) is far below a bfloat16 result's own rounding of 2^-8. A binary16 result's is
 //     2^-11: one part more than doubled its error, as p s multiplies codes of mean 7.5 that the biases take back out (64
 //     to 20000 positions of like weight: 4.3e-4 to 4.9e-4 in one part, 2.0e-4 to 2.2e-4 in two, which is the rounding
-//     of the result; 12 requests of 5 queries, 64 columns: 38.3 us in one part, 42.7 us in two).
+//     of the result; 12 requests of 5 queries, 64 columns: 37 us in one part, 41 us in two; the long request of the
+//     file's head 72 and 97 us).
 //   normal: codes as normal numbers. Sums of products drop what lies below 2^-24 of the largest exponent among them, and
 //     a subnormal counts there as 2^10 times what it is: with codes in place a binary32 result was up to 4e-5 off.
 template <typename T>
@@ -812,8 +819,8 @@ AttnPlan plan_attn(const fmoe_kv_cache& c, const fmoe_attn_desc& a, int sms) {
   const int terms = terms_of(a.dtype), groups = c.dim / 64;
   // as few warps as can carry the rows, and then as few tiles a warp as that takes: what unpacking codes costs is
   // shared by more rows, and more warps have positions of their own. 12 requests of 5 queries, 4 heads a kv head of
-  // 64: 37.4 us by three tiles of one warp, 41.2 by three warps; 16 heads a kv head of 256, 262144 positions: 71.3
-  // us by two tiles, 76.6 by two warps.
+  // 64, binary16: 40.5 us by three tiles of one warp, 47.2 by three warps; 16 heads a kv head of 256, 262144 positions:
+  // 72.5 us by two tiles, 77.5 by two warps.
   const long long warps = (tiles + most_tiles(groups) - 1) / most_tiles(groups);
   p.row_tiles = (int)((tiles + warps - 1) / warps);
   p.row_warps = 1;
@@ -825,8 +832,7 @@ AttnPlan plan_attn(const fmoe_kv_cache& c, const fmoe_attn_desc& a, int sms) {
   p.q_offset = shared.q_offset, p.smem = shared.bytes;
   const long long units = (long long)c.heads * p.row_blocks;
   const long long items = c.n_seqs * units, passes = std::max(1, (a.max_len + kStage - 1) / kStage);
-  // Short sequences: a CTA takes one item, whatever its length, and nothing is left to join. One request of 777
-  // positions, 32 query heads and 4 kv heads of 128 takes 14.3 us so, 14.7 us shared by 25 CTAs and joined.
+  // Short sequences (kShort): a CTA takes one item, whatever its length, and nothing is left to join.
   // Else as many CTAs as are resident at once, or enough that every ring has a pass.
   p.by_item = passes <= kShort * rings;
   p.ctas = (int)(p.by_item ? items : std::min<long long>((items * passes + rings - 1) / rings, (long long)at_once * sms));

@@ -10,8 +10,8 @@
 //
 // A decode step reads and writes every state once (8 bytes an entry for about 6 flops): it is bound
 // by HBM. 32 columns keep 128-byte row segments and give one sequence of 64 heads 256 CTAs. Measured, 64 heads of
-// 128 x 128, bf16: 128 requests 175 us, 94 % of the copy rate; one request 3.5 us, a launch with slot, state and
-// sums one after another in it.
+// 128 x 128, bf16: 128 requests 175 to 187 us, 94 to 88 % of the copy rate, by the machine; one request 4.1 us, a launch
+// with slot, state and sums one after another in it.
 #include "api.h"
 #include "mixer.h"
 

@@ -19,9 +19,10 @@
 // Loops over blocks of 32 columns keep the code small: unrolled, it outgrew the instruction caches and every
 // phase waited for its instructions (8 prompts, 8192 tokens, 64 heads: 614 us unrolled, 483 us in loops).
 //
-// Measured, 64 heads of 128 x 128: 8 packed prompts of 8192 tokens in all 453 us (114 TFLOP/s of the recurrence's
-// own operations), one of 16384 tokens 1650 us, one of 333 tokens 47 us. Latency bounds it, not a rate: a chunk is
-// 6.4 us of products and of trips between tensor memory and registers that wait for one another, about as much in
+// Measured, 64 heads of 128 x 128: 8 packed prompts of 8192 tokens in all 450 to 575 us by their lengths, and by their
+// order, in which the blocks start (the same eight lengths falling 414 us, mixed 454, rising 521: the longest runs alone
+// at the end); one of 16384 tokens, binary16, 1725 us, one of 333 tokens 48 us. Latency bounds it, not a rate: a chunk
+// is 6.7 us of products and of trips between tensor memory and registers that wait for one another, about as much in
 // the chain as in the preparing warps, and one sequence has no more than a CTA a head, 64 for 148 SMs.
 //
 // Precision. Operands are binary16 with a power of two taken out of every row: keys and queries (16-bit

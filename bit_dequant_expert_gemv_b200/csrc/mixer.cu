@@ -123,8 +123,8 @@ int fmoe_delta_chunk(const fmoe_delta_desc* d, const int32_t* cu_seqlens, int n,
   const DeltaRun r{*d, cu_seqlens, fresh, n, n_tokens, dev->err};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // A chunk costs as much however few of its 64 tokens there are. Recurrent and chunked form in us, 32 heads of
-  // 128 x 128: sequences of 8 tokens 9.1 and 15.2 (one), 27 and 29 (8 of them), 188 and 220 (64); of 16 tokens
-  // 15.6 and 15.1, 49 and 29, 346 and 221; of 64 tokens 55 and 15, 166 and 29, 1305 and 224.
+  // 128 x 128: sequences of 8 tokens 9.6 and 15.0 (one), 27 and 30 (8 of them), 191 and 225 (64); of 16 tokens
+  // 16.4 and 15.7, 50 and 29, 352 and 226; of 64 tokens 57 and 16, 190 and 33, 1322 and 230.
   const bool chunked = d->dtype != FMOE_F32 && max_len >= 16;
   return launched(chunked ? launch_delta_chunk(r, st) : launch_delta_recurrent(r, st), "delta chunk launch");
 }

@@ -1,5 +1,5 @@
 // mma.cuh — warp matrix instructions: m16n8k16 products of binary16 with binary32 sums, and the
-// loads and transposes that feed them. With g = lane / 4 and c = lane % 4 a thread holds
+// copies and transposes that feed them. With g = lane / 4 and c = lane % 4 a thread holds
 //   A (16 x 16): a[0] row g, columns 2c, 2c+1; a[1] row g+8; a[2] row g, columns 2c+8, 2c+9; a[3] row g+8
 //   B (16 x 8):  b[0] rows 2c, 2c+1 of column g; b[1] rows 2c+8, 2c+9
 //   C (16 x 8):  c[0], c[1] row g, columns 2c, 2c+1; c[2], c[3] row g+8

@@ -403,7 +403,8 @@ size_t fmoe_kv_block_bytes(int page_size, int dim);
  * token is written). Two tokens of a call must not share a place.
  * Rotation, over the first 2*n_freq columns of a row, pairs (i, i+n_freq), or (2i, 2i+1) when
  * interleaved: (a, b) -> (a cos - b sin, b cos + a sin) with the angle position * inv_freq[i]
- * (exact product and cosine in binary64, the rest in binary32). */
+ * (product and cosine in binary64: the product is exact below position 2^29; the rest in
+ * binary32). */
 typedef struct fmoe_kv_tokens {
     int dtype;               /* of q, k, v, q_out                                     */
     int n_tokens;
