@@ -598,8 +598,9 @@ __device__ __forceinline__ void chain(const DeltaRun& r, uint8_t* smem, int seq,
   const uint32_t lanes = tmem + (uint32_t)((row & ~31) << 16);
   float* const state = d.state + slot * d.state_stride + (int64_t)head * DK * d.dim_v + row;
   float2* const scales = reinterpret_cast<float2*>(smem + M::kRows);
-  // The state is S times `unit`, a power of two that keeps S inside binary16's range; what the last chunk left to
-  // be done to S is S = grow * S + increment.
+  // The state is S times `unit`, a power of two that keeps S inside binary16's range (2^-40 at least, so that values of
+  // 2^80 may still follow; binary16's last place is then 2^-65); what the last chunk left to be done to S is
+  // S = grow * S + increment.
   float unit = 1.f, grow = 1.f, top = 0.f;
   {
     const bool load = real && !(r.fresh && r.fresh[seq]);

@@ -360,7 +360,7 @@ int fmoe_delta_step(const fmoe_delta_desc* d, int n, void* stream);
  * inputs with max_len >= 16 take the chunked form (64 tokens at a time on the tensor cores), all
  * else the recurrent form; a longer sequence than max_len is still computed. The chunked form holds
  * what a column of the state meets within 64 tokens (values, and the state's answers to the keys)
- * to 22 bits down to 2^-15 of the largest of them and to 2^-39 of it below: a state that is more
+ * to 22 bits down to 2^-15 of the largest of them and to 2^-39 of it below (2^-65 at best): a state that is more
  * than 2^20 times the values and is forgotten within one chunk leaves no exact ones; the
  * recurrent form (max_len 0) does. In both forms a key, gate or step size that is not finite (a
  * gate: whose exponential is not) leaves its token's results and the later ones of its head, and

@@ -51,11 +51,13 @@ def delta_parts(q, k, v, g, beta, S, scale, eps=1e-6):
     return out, S, us, old, new
 
 
-def check_tokens(got, got_state, x, lens, dtype, l=64):  # noqa: E741
+def check_tokens(got, got_state, x, lens, dtype):
     """Every token and head by itself. Terms: the result's rounding; M and U in binary16 (2^-12 each) for a bfloat16
     result, in 22 bits (2^-21 for both) for a binary16 one; the state and the sums, as state_bound; and the limit that
     fmoe.h gives: 2^-39 of the largest that a column meets within the chunk, 64 of them in a sum, in each of the right-
-    hand side, U, and T."""
+    hand side, U, and T; and 2^-65 in every entry of the state, before every chunk. That is up to sqrt(dk) 2^-65 in k~ S,
+    so in each token's right-hand side, and a token adds as much (times beta <= 1 and |k~| <= 1) to the error of its
+    column of the state, which the rule contracts: sqrt(dk) 2^-65 a token so far, times sqrt(dv) for all columns."""
     q, k, v, g, beta = (ref.f64(t) for t in x[:5])
     state0, slots, cu = ref.f64(x[5]), x[6].tolist(), x[7].tolist()
     dk = k.shape[-1]
@@ -65,15 +67,16 @@ def check_tokens(got, got_state, x, lens, dtype, l=64):  # noqa: E741
         b = cu[i]
         out, S, us, old, new = delta_parts(q[b:b + n], k[b:b + n], v[b:b + n], g[b:b + n], beta[b:b + n], state0[slots[i]], scale)
         for t in range(n):
-            c = t - t % l
-            top = np.maximum(np.abs(us[c:c + l]), np.abs(v[b + c:b + n][:l])).max(0)  # [heads, columns]
+            c = t - t % 64
+            top = np.maximum(np.abs(us[c:c + 64]), np.abs(v[b + c:b + n][:64])).max(0)  # [heads, columns]
             bound = (eps * np.linalg.norm(out[t], axis=-1) + operand * np.linalg.norm(new[t], axis=-1)
                      + 4 * state_bound(dk) * (np.linalg.norm(old[t], axis=-1) + np.linalg.norm(new[t], axis=-1))
-                     + scale * 3 * 64 * 2.0 ** -39 * np.linalg.norm(top, axis=-1))
+                     + scale * (3 * 64 * 2.0 ** -39 * np.linalg.norm(top, axis=-1) + (t + 2) * 2.0 ** -65 * (dk * v.shape[-1]) ** 0.5))
             off = np.linalg.norm(got[b + t] - out[t], axis=-1)
             assert (off <= bound).all(), (i, t, (off / bound).max())
-        top = np.abs(us[n - 1 - (n - 1) % l:]).max(0)
-        bound = 2 * state_bound(dk) * np.linalg.norm(S, axis=(1, 2)) + 3 * 64 * 2.0 ** -39 * np.linalg.norm(top, axis=-1)
+        top = np.abs(us[n - 1 - (n - 1) % 64:]).max(0)
+        bound = (2 * state_bound(dk) * np.linalg.norm(S, axis=(1, 2)) + 3 * 64 * 2.0 ** -39 * np.linalg.norm(top, axis=-1)
+                 + (n + 1) * 2.0 ** -65 * (dk * v.shape[-1]) ** 0.5)
         off = np.linalg.norm(got_state[slots[i]] - S, axis=(1, 2))
         assert (off <= bound).all(), (i, "state", (off / bound).max())
 
@@ -111,6 +114,18 @@ def test_delta_chunk_stretches_by_token(fmoe, decay):
     x[2] = v
     state = x[5].clone()
     out = fmoe.delta_chunk(*x[:5], state, x[7], 700, slots=x[6])
+    assert fmoe.sync_status() == 0
+    check_tokens(out, state, x, lens, torch.bfloat16)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -45, 2.0 ** 60])
+def test_delta_chunk_of_any_size(fmoe, size):
+    """Values and states far from 1 in size."""
+    lens = [200, 65]
+    x = list(delta_inputs(lens, 2, 2, 128, 64, torch.bfloat16, 23))
+    x[2], x[5] = x[2] * size, x[5] * size
+    state = x[5].clone()
+    out = fmoe.delta_chunk(*x[:5], state, x[7], 200, slots=x[6])
     assert fmoe.sync_status() == 0
     check_tokens(out, state, x, lens, torch.bfloat16)
 
@@ -464,6 +479,10 @@ def test_results_on_another_stream(fmoe):
     for call in calls:
         state.copy_(x[5])
         want = call(None).clone()
+        state.copy_(x[5])
+        out = call(0)  # the default stream by its handle, here the current one
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
         for s in (st, st.cuda_stream):
             state.copy_(x[5])
             torch.cuda.synchronize()
