@@ -381,8 +381,6 @@ def _empty(like, shape, dtype, stream):
     written by what that stream has yet to run: another stream's result is allocated on that one, and outlives the
     current one's use of it."""
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
@@ -431,7 +429,7 @@ def _delta(dev, q, k, v, g, beta, state, n, slots, scale, l2norm, eps, out, stre
         raise ValueError("state must be float32 [slots, heads, dim_k, dim_v], contiguous within a slot")
     sp = _array(slots, torch.int32, dev, "slots", n)
     if out is None:
-        out = _empty(v, shape, dt, stream)
+        out = torch.empty(shape, dtype=dt, device=v.device) if stream is None else _empty(v, shape, dt, stream)
     ov = _rows(out, dt, dev, "out", shape)
     return out, DeltaDesc(heads_k, heads_v, dim_k, dim_v, code, l2norm, eps,
                           dim_k ** -0.5 if scale is None else scale, *qv, *kv, *vv, g.data_ptr(),
@@ -516,7 +514,7 @@ def kv_append(k, v, positions, pages, page_table, inv_freq, seq=None, q=None, q_
         if q_shape != (tokens, heads_q, dim):
             raise ValueError(f"q has shape {tuple(q_shape)}, expected ({tokens}, heads, {dim})")
         if q_out is None:
-            q_out = _empty(k, q_shape, dt, stream)
+            q_out = torch.empty(q_shape, dtype=dt, device=k.device) if stream is None else _empty(k, q_shape, dt, stream)
         ov = _rows(q_out, dt, dev, "q_out", q_shape)
     a = KvTokens(code, tokens, *kv, *vv, pp, sp, fp, n_freq, interleaved, heads_q, *qv, *ov)
     _call("fmoe_kv_append", dev, stream, c, a)
@@ -532,8 +530,10 @@ def kv_read(pages, page_table, positions, dim: int, seq=None, dtype=None, k=None
     tokens = positions.numel()
     shape = (tokens, c.heads, dim)
     dt = dtype if dtype is not None else torch.bfloat16 if k is None else k.dtype
-    k = _empty(pages, shape, dt, stream) if k is None else k
-    v = _empty(pages, shape, dt, stream) if v is None else v
+    if k is None:
+        k = torch.empty(shape, dtype=dt, device=pages.device) if stream is None else _empty(pages, shape, dt, stream)
+    if v is None:
+        v = torch.empty(shape, dtype=dt, device=pages.device) if stream is None else _empty(pages, shape, dt, stream)
     pp = _array(positions, torch.int32, dev, "positions", tokens)
     sp = _array(seq, torch.int32, dev, "seq", tokens)
     _call("fmoe_kv_read", dev, stream, c, pp, sp, tokens, _dtype(dt), View(*_rows(k, dt, dev, "k", shape)),
@@ -551,7 +551,8 @@ def attn_q4(q, pages, page_table, lens, max_len: int, cu_q=None, max_q: int = 1,
     qv = _rows(q, dt, dev, "q")
     tokens, heads, dim = shape = q.shape
     c = _cache(dev, pages, page_table, dim)
-    out = _empty(q, shape, dt, stream) if out is None else out
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=q.device) if stream is None else _empty(q, shape, dt, stream)
     ov = _rows(out, dt, dev, "out", shape)
     lp = _array(lens, torch.int32, dev, "lens", c.n_seqs)
     cp = _array(cu_q, torch.int32, dev, "cu_q", c.n_seqs + 1)
