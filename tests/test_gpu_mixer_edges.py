@@ -145,6 +145,55 @@ def test_delta_chunk_binary16_results(fmoe, lens, dk, dv):
     flips(out, np.concatenate(want), torch.float16, state_bound(dk), "out")
 
 
+@pytest.mark.parametrize("dtype,most", [("bf16", 70), ("fp32", 70), ("bf16", 0)])
+def test_delta_chunk_padding_layers_and_broadcast(fmoe, dtype, most):
+    """A padded sequence and one of a bad slot among others, states that are one layer's slice of a larger array, gates that
+    are slices, a key shared by all heads and tokens: what contiguous copies give, and nothing else written."""
+    lens, hv, d = [70, 30, 64, 9], 4, 64
+    x = list(delta_inputs(lens, 2, hv, d, d, DT[dtype], 60))
+    t = sum(lens)
+    layers = 0.3 * torch.randn(6, 3, hv, d, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(61))
+    gates = torch.randn(t, 3 * hv, device="cuda", generator=torch.Generator(device="cuda").manual_seed(62))
+    gates[:, :hv] = -gates[:, :hv].abs()
+    gates[:, hv:2 * hv].sigmoid_()
+    k = x[1][:1, :1].expand(t, 2, d)
+    slots = torch.tensor([4, -1, 0, 6], dtype=torch.int32, device="cuda")
+    before, out = layers.clone(), torch.full((t, hv, d), 7.0, dtype=DT[dtype], device="cuda")
+    fmoe.delta_chunk(x[0], k, x[2], gates[:, :hv], gates[:, hv:2 * hv], layers[:, 1], x[7], most, slots=slots, out=out)
+    assert fmoe.sync_status() == fmoe.FMOE_ERR_INDEX and "slot" in fmoe.last_error()
+    state = before[:, 1].contiguous()
+    good = torch.tensor([4, 5, 0, 2], dtype=torch.int32, device="cuda")
+    want = fmoe.delta_chunk(x[0].contiguous(), k.contiguous(), x[2].contiguous(), gates[:, :hv].contiguous(),
+                            gates[:, hv:2 * hv].contiguous(), state, x[7], most, slots=good)
+    assert fmoe.sync_status() == 0
+    for i, (a, b) in enumerate(zip(x[7].tolist(), x[7].tolist()[1:])):
+        assert torch.equal(out[a:b], want[a:b]) if i in (0, 2) else (out[a:b] == 7).all()
+    for i in range(6):
+        assert torch.equal(layers[i, 1], state[i] if i in (4, 0) else before[i, 1])
+    assert torch.equal(layers[:, 0], before[:, 0]) and torch.equal(layers[:, 2], before[:, 2])
+
+
+@pytest.mark.parametrize("dtype,most", [("bf16", 70), ("bf16", 0)])
+def test_delta_offsets_beyond_32_bits(fmoe, dtype, most):
+    """States and rows whose elements lie beyond 2^31."""
+    hv, d, step, t = 64, 128, 1 << 25, 70
+    wide = torch.empty(3, t * step // 2, dtype=torch.bfloat16, device="cuda")  # 3 x 2.3 GB: rows step / 2 apart, q, k, v
+    x = list(delta_inputs([t], 2, hv, d, d, torch.bfloat16, 63))
+    far = [torch.as_strided(wide.view(-1), (t, a.shape[1], d), (step * 3 // 2, d, 1), i * 16384) for i, a in enumerate(x[:3])]
+    for a, b in zip(far, x[:3]):
+        a.copy_(b)
+    assert (t - 1) * step * 3 // 2 > 2 ** 31
+    state = torch.empty(2060, hv, d, d, device="cuda")  # 8.6 GB
+    slots = torch.tensor([2059], dtype=torch.int32, device="cuda")
+    state[2059] = x[5][0]
+    few = x[5][:1].clone()
+    want = fmoe.delta_chunk(*x[:5], few, x[7], most)
+    out = torch.as_strided(wide.view(-1), (t, hv, d), (step * 3 // 2, d, 1), 3 * 16384)
+    fmoe.delta_chunk(*far, *x[3:5], state, x[7], most, slots=slots, out=out)
+    assert fmoe.sync_status() == 0
+    assert torch.equal(out, want) and torch.equal(state[2059], few[0])
+
+
 NAN, INF = float("nan"), float("inf")
 
 
@@ -241,6 +290,39 @@ def test_append_not_finite(fmoe, dtype, d):
     for clean, got in zip(*held):
         assert not torch.isfinite(got[hit]).any()
         assert torch.equal(got[~hit], clean[~hit])
+
+
+def test_cache_beyond_32_bits(fmoe):
+    """Pages that lie beyond 2^32 bytes, through a slice of a wider table: as in a small cache."""
+    d, ps, hkv, n = 256, 1024, 8, 1500
+    gen = torch.Generator(device="cuda").manual_seed(64)
+    kv = torch.randn(n, 2 * hkv, d, generator=gen, device="cuda").to(torch.bfloat16)
+    q = torch.randn(1, 16, d, generator=gen, device="cuda").to(torch.bfloat16)
+    P, S = torch.arange(n, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    L = torch.tensor([n], dtype=torch.int32, device="cuda")
+    got = []
+    for pages, ids in ((fmoe.kv_pages(2, hkv, d, ps), [1, 0]),
+                       (torch.empty(2000, hkv, fmoe.kv_block_bytes(ps, d), dtype=torch.uint8, device="cuda"), [1999, 1960])):
+        wide = torch.full((1, 9), -1, dtype=torch.int32, device="cuda")
+        wide[0, 4:6] = torch.tensor(ids, dtype=torch.int32)
+        table = wide[:, 4:6]
+        fmoe.kv_append(kv[:, :hkv], kv[:, hkv:], P, pages, table, torch.zeros(0, device="cuda"), seq=S)
+        got.append([*fmoe.kv_read(pages, table, P, d, seq=S), fmoe.attn_q4(q, pages, table, L, n)])
+    assert pages.stride(0) * 1960 > 2 ** 32 and fmoe.sync_status() == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_append_padding_leaves_queries(fmoe):
+    d, ps = 64, 16
+    x = torch.randn(4, 4, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(65))
+    pages, table = fmoe.kv_pages(4, 1, d, ps), torch.arange(4, dtype=torch.int32, device="cuda")[:, None]
+    P = torch.tensor([3, -1, 0, -7], dtype=torch.int32, device="cuda")
+    out = torch.full((4, 2, d), 7.0, device="cuda")
+    fmoe.kv_append(x[:, 2:3], x[:, 3:], P, pages, table, torch.ones(8, device="cuda"), q=x[:, :2], q_out=out)
+    assert fmoe.sync_status() == 0
+    assert (out[[1, 3]] == 7).all() and not (out[[0, 2]] == 7).any()
+    assert not pages[[1, 3]].any() and pages[0].any() and pages[2].any()
 
 
 # ------------------------------------------------------------------------------------------------ attention
